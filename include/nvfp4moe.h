@@ -101,6 +101,11 @@ enum {
 #define NVFP4_SF_TILED 1
 #define NVFP4_SF_TILED_ROWS 2
 
+/* Element types of the entry points that take one. */
+#define NVFP4MOE_BF16 0
+#define NVFP4MOE_F16 1
+#define NVFP4MOE_F32 2
+
 /* Routed rows (T * k) up to which moe_dispatch and moe_dispatch_static do the
  * quantize + scatter inside their cooperative kernel; above, a second kernel
  * does it (measured faster there). */
@@ -478,6 +483,98 @@ int moe_forward_static(const void* x, const float* router_logits, int64_t T, int
                        const uint8_t* w1_sf, const float* gs_w1, const uint8_t* w2_codes,
                        const uint8_t* w2_sf, const float* gs_w2, const float* gs_h, void* y,
                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Tokens in expert order and back, with their gradients, for rows of any width
+ * K in BF16, F16 or F32 (`type`: NVFP4MOE_BF16, _F16 or _F32). With p(t, j) =
+ * flat_to_perm[t*k + j], the row of slot j of token t (moe_permute's inverse
+ * permutation, or any other placement in n_rows rows without a row named
+ * twice):
+ *   moe_sort_tokens             rows[p(t,j)] = w[t,j] * x[t]
+ *   moe_sort_tokens_backward    dx[t] = sum_j w[t,j] * d_rows[p(t,j)]
+ *                               d_w[t,j] = <x[t], d_rows[p(t,j)]>
+ *   moe_unsort_tokens           y[t] = sum_j w[t,j] * rows[p(t,j)]
+ *   moe_unsort_tokens_backward  d_rows[p(t,j)] = w[t,j] * dy[t]
+ *                               d_w[t,j] = <dy[t], rows[p(t,j)]>
+ * Sums and dot products in f32, in a fixed order, rounded once.
+ *   topk_w  (T, k) f32, or NULL: all weights 1.
+ *   d_w     (T, k) f32, given together with the other operand of its dot
+ *           products (x, rows) and topk_w, or all NULL: not computed.
+ *   A negative flat_to_perm entry is a dropped slot: nothing is written for it
+ *   and it adds nothing (d_w 0). An entry >= n_rows is taken the same way and
+ *   records NVFP4MOE_ERR_INVALID in the device status word. Rows that no entry
+ *   names are not written.
+ * Leading dimensions in elements, >= K. Accesses are 16 bytes wide where all
+ * operands' rows start on 16-byte boundaries, else one element wide. Inputs
+ * and outputs must not overlap. Requires 1 <= k <= 16, T * k < 2^31.
+ * Errors: INVALID, UNSUPPORTED, LAUNCH.
+ */
+int moe_sort_tokens(const void* x, int type, int64_t T, int64_t K, int64_t ldx, const int32_t* flat_to_perm, int k,
+                    const float* topk_w, void* rows, int64_t n_rows, int64_t ldr, void* stream);
+int moe_sort_tokens_backward(const void* d_rows, int type, int64_t n_rows, int64_t K, int64_t ldr,
+                             const int32_t* flat_to_perm, int64_t T, int k, const float* topk_w, const void* x,
+                             int64_t ldx, void* dx, int64_t lddx, float* d_w, void* stream);
+int moe_unsort_tokens(const void* rows, int type, int64_t n_rows, int64_t K, int64_t ldr,
+                      const int32_t* flat_to_perm, int64_t T, int k, const float* topk_w, void* y, int64_t ldy,
+                      void* stream);
+int moe_unsort_tokens_backward(const void* dy, int type, int64_t T, int64_t K, int64_t lddy,
+                               const int32_t* flat_to_perm, int k, const float* topk_w, const void* rows,
+                               int64_t ldr, void* d_rows, int64_t n_rows, int64_t lddr, float* d_w, void* stream);
+
+/*
+ * 8-bit block-scaled operands: E4M3 codes, one byte an element, row-major, and
+ * f32 scales, value = code * scale. An activation has one scale per row and
+ * 128 elements, (rows, ceil(K/128)) row-major; a weight one per 128 x 128
+ * block, (E, ceil(N/128), ceil(K/128)); the last blocks may be short.
+ * Rule, every step one f32 operation: scale = amax / 448, code = E4M3 of
+ * x * (448 / amax) rounded to nearest even. A block whose amax is below 2^-100
+ * has scale 0 and codes 0. A block that holds an infinity or a NaN has an
+ * infinite or NaN scale, and all of it reads back as NaN.
+ *
+ * fp8_quantize -- rows of x (rows, K), BF16, F16 or F32 by `type`.
+ *   flat_to_perm  NULL: output row r is source row r. Or (rows, k) int32 row
+ *                 numbers, as moe_permute's: source row r is quantized once
+ *                 and written to each of its k rows (negative: dropped; >=
+ *                 out_rows: dropped, and NVFP4MOE_ERR_INVALID in the device
+ *                 status word). Rows that no entry names are not written.
+ *   codes (out_rows, K) bytes, 16-byte aligned; sf (out_rows, ceil(K/128)) f32.
+ * fp8_swiglu_quantize -- the same of h = silu(gate) * up, silu(g) =
+ *   g / (1 + exp(-g)) in f32, for rows [gate 0..I-1 | up 0..I-1] of gate_up.
+ * fp8_quantize_weight -- w (E, N, K), rows ldw elements apart, into 128 x 128
+ *   blocks: codes (E, N, K) bytes, sf (E, ceil(N/128), ceil(K/128)) f32.
+ * Sources: base address and row stride multiples of 16 bytes; K (I) a multiple
+ * of 16. 1 <= k <= 16. Errors: INVALID, UNSUPPORTED, LAUNCH.
+ */
+int fp8_quantize(const void* x, int type, int64_t rows, int64_t K, int64_t ldx, const int32_t* flat_to_perm, int k,
+                 int64_t out_rows, uint8_t* codes, float* sf, void* stream);
+int fp8_swiglu_quantize(const void* gate_up, int type, int64_t rows, int64_t I, int64_t ld, uint8_t* codes, float* sf,
+                        void* stream);
+int fp8_quantize_weight(const void* w, int type, int64_t E, int64_t N, int64_t K, int64_t ldw, uint8_t* codes,
+                        float* sf, void* stream);
+
+/*
+ * fp8_linear, fp8_grouped_gemm -- products of 8-bit block-scaled operands:
+ *   C[m, n] = sum_b a_sf[m, b] * w_sf[e, n/128, b] * sum_{k in block b} A[m, k] * W[e, n, k]
+ * f32 accumulation, rounded once to c_type (BF16, F16 or F32).
+ *   A        (M, K) codes, rows lda bytes apart; a_sf (M, ceil(K/128)).
+ *   W        (E, N, K) codes, rows ldw bytes apart (expert e's first row is row
+ *            e*N); w_sf (E, ceil(N/128), ceil(K/128)). fp8_linear: E = 1.
+ *   offsets  (E + 1) int32 (device): rows [offsets[e], offsets[e+1]) of A and C
+ *            belong to expert e (compact rows, moe_permute's offsets). Bounds
+ *            are clamped to [0, M] and to ascending order; rows of no group
+ *            are not written.
+ *   C        (M, N), leading dimension ldc elements. Stores are 32 bytes wide
+ *            where C's rows start on 32-byte boundaries, else one element.
+ * The gradient with respect to A is the same product with W's codes and
+ * scales transposed. Requires K >= 1, 1 <= E <= 1024; lda and ldw multiples of
+ * 16, codes 16-byte aligned. Errors: INVALID, UNSUPPORTED, LAUNCH; a wait that
+ * runs out on the device is reported by nvfp4moe_last_device_status.
+ */
+int fp8_linear(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, const uint8_t* w_codes,
+               const float* w_sf, int64_t N, int64_t K, int64_t ldw, void* c, int c_type, int64_t ldc, void* stream);
+int fp8_grouped_gemm(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, const uint8_t* w_codes,
+                     const float* w_sf, const int32_t* offsets, int E, int64_t N, int64_t K, int64_t ldw, void* c,
+                     int c_type, int64_t ldc, void* stream);
 
 /* Waits for `stream`, then reads and clears the device status word that the
  * GEMM and fused-front kernels set when a bounded wait runs out (and

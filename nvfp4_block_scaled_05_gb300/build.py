@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
-SOURCES = ["quantize.cu", "routing.cu", "front.cu", "gemm.cu", "api.cu", "layout.cu"]
+SOURCES = ["quantize.cu", "routing.cu", "front.cu", "gemm.cu", "api.cu", "layout.cu", "sorted.cu",
+           "fp8_quantize.cu", "fp8_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

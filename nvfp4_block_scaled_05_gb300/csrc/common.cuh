@@ -44,6 +44,12 @@ uint64_t wait_limit_ns();
 int device_num_sms();
 int test_stall_on();   // failure-path test hook (nvfp4moe_set_test_stall)
 
+// Tensor map (defined with the GEMM) of `rows` rows of row_bytes bytes,
+// ld_bytes apart (a multiple of 16): a box of 128 bytes x box_rows rows with
+// the 128-byte swizzle; bytes past a row's end and past the last row read 0.
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int64_t ld_bytes,
+                    int box_rows);
+
 // Fused front (front.cu): routing, permutation, quantization and scatter in
 // one cooperative kernel; gs_x null = the global scale is computed from max|x|
 // (and written to gs_out when that is not null). moe_front_fits: whether T
@@ -474,7 +480,7 @@ __device__ __forceinline__ void tc_ld64_wait(uint32_t taddr, uint32_t (&r)[64]) 
       : "memory");
 }
 
-// ---- thread-block clusters of two CTAs (the 2-SM MMA pairs)
+// ---- thread-block clusters (of two CTAs: the 2-SM MMA pairs)
 
 // Rank of this CTA in its cluster.
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -527,6 +533,41 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+
+// Bounded wait. Returns false on timeout (after raising the abort flag, the
+// pair peer's abort flag when peer_abort != 0, and the device status) or when
+// another role has aborted. kCluster: the barrier is arrived on from the pair
+// peer (acquire at cluster scope).
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             uint64_t limit_ns, int* status, int site, uint32_t peer_abort = 0) {
+  auto probe = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (probe()) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (probe()) return true;
+    if ((it & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > limit_ns) {
+        *abort_flag = 1;
+        if (peer_abort) st_shared_cluster_u32(peer_abort, 1u);
+        if (atomicCAS(&status[0], 0, NVFP4MOE_ERR_DEVICE_TIMEOUT) == 0) status[1] = site;
+        return false;
+      }
+    }
+  }
+}
+
+// Wait used while shutting down: ignores the abort flag, fixed bound.
+template <bool kCluster = false>
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+    if (global_timer_ns() - t0 > kDrainLimitNs) return;
+  }
 }
 
 // Tensor memory of a CTA pair: one warp of EACH of the two CTAs executes the

@@ -79,7 +79,6 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC_COLS = BN;             // one f32 accumulator of 256 columns
 constexpr uint32_t SFB_SLOT = 32;
 constexpr uint32_t SFA_SLOT = 16;
-constexpr uint64_t kDrainLimitNs = 1000000000ull;
 constexpr uint64_t kPairCopyDrainNs = 2000000ull;   // 2 ms
 
 // Shared- and tensor-memory plan of one CTA. kPair: the CTA is one half of a
@@ -164,39 +163,6 @@ struct Sched {
     ncols = min(BN, N - nb * BN);   // 256, or 128 for the last tile when N % 256 == 128
   }
 };
-
-// Bounded wait. Returns false on timeout (after raising the abort flag, the
-// pair peer's abort flag when peer_abort != 0, and the device status) or when
-// another role has aborted. kCluster: the barrier is arrived on from the pair
-// peer (acquire at cluster scope).
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             uint64_t limit_ns, int* status, int site, uint32_t peer_abort = 0) {
-  auto probe = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (probe()) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (probe()) return true;
-    if ((it & 15u) == 0) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
-        *abort_flag = 1;
-        if (peer_abort) st_shared_cluster_u32(peer_abort, 1u);
-        if (atomicCAS(&status[0], 0, NVFP4MOE_ERR_DEVICE_TIMEOUT) == 0) status[1] = site;
-        return false;
-      }
-    }
-  }
-}
-
-// Wait used while shutting down: ignores the abort flag, fixed bound.
-template <bool kCluster = false>
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
-    if (global_timer_ns() - t0 > kDrainLimitNs) return;
-  }
-}
 
 // silu(g) = g / (1 + exp(-g)) with the hardware exponential and reciprocal
 // (a few ulp; h is requantized to 4 bits right after).
@@ -751,39 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
-// Rows of `row_bytes` bytes (K/2 codes), box of 128 bytes x box_rows rows,
-// 128-byte swizzle.
-bool make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 int g_num_sms = 0;
 uint64_t g_wait_limit_ns = 4000000000ull;
 int g_test_stall = 0;
@@ -838,8 +771,8 @@ int launch_grouped(const uint8_t* a_codes, int64_t a_rows, const uint8_t* b_code
   CUtensorMap ma[4], mb;
   const int boxes[4] = {16, 32, 64, 128};
   for (int i = 0; i < 4; ++i)
-    if (!make_codes_map(&ma[i], a_codes, a_rows, K / 2, boxes[i])) return NVFP4MOE_ERR_INVALID;
-  if (!make_codes_map(&mb, b_codes, (int64_t)p.E * N, K / 2, pair ? BN / 2 : BN)) return NVFP4MOE_ERR_INVALID;
+    if (!make_codes_map(&ma[i], a_codes, a_rows, K / 2, K / 2, boxes[i])) return NVFP4MOE_ERR_INVALID;
+  if (!make_codes_map(&mb, b_codes, (int64_t)p.E * N, K / 2, K / 2, pair ? BN / 2 : BN)) return NVFP4MOE_ERR_INVALID;
   int* status = nullptr;
   if (cudaGetSymbolAddress(reinterpret_cast<void**>(&status), g_status) != cudaSuccess)
     return NVFP4MOE_ERR_LAUNCH;
@@ -894,6 +827,32 @@ int check_common(const uint8_t* a_codes, const uint8_t* a_sf, const float* gs_a,
 }
 
 }  // namespace
+
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int64_t ld_bytes,
+                    int box_rows) {
+  using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                     CUtensorMapFloatOOBfill);
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld_bytes};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
 
 int* device_status_word() {
   int* status = nullptr;

@@ -1,0 +1,318 @@
+// Tokens in expert order and back, with routing weights, and the gradients.
+//
+// With p(t, j) = flat_to_perm[t * k + j], the row of slot j of token t:
+//   sort             rows[p(t,j)] = w[t,j] * x[t]
+//   sort backward    dx[t] = sum_j w[t,j] * d_rows[p(t,j)],  d_w[t,j] = <x[t], d_rows[p(t,j)]>
+//   unsort           y[t]  = sum_j w[t,j] * rows[p(t,j)]
+//   unsort backward  d_rows[p(t,j)] = w[t,j] * dy[t],        d_w[t,j] = <dy[t], rows[p(t,j)]>
+// Two kernels do all four: one spreads a token row over its k rows, the other
+// sums the k rows of a token; each takes the dot products of d_w along, from
+// data that it reads anyway (the sum) or that the spread reads beside it.
+// Everything is read once and written once, so HBM bounds them.
+#include "common.cuh"
+
+#include <cuda_fp16.h>
+
+namespace nvfp4moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 16;
+
+struct Args {
+  const void* token_in;    // spread: the token rows; collect with dots: the token rows of the dots
+  void* token_out;         // collect: the sums
+  int64_t ldt_in, ldt_out;
+  const void* rows_in;     // collect: the rows; spread with dots: the rows of the dots
+  void* rows_out;          // spread: the rows written
+  int64_t ldr_in, ldr_out;
+  int64_t n_rows;          // rows that flat_to_perm may name
+  const int32_t* f2p;
+  const float* w;          // (T, k) or null: all ones
+  float* d_w;              // (T, k), with dots
+  int64_t T, K;
+  int k;
+  int* status;
+};
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<__half> {
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+template <> struct Elem<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+
+// V consecutive elements as one access (V * sizeof(T) is 16 bytes, or V is 1).
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+  T e[V];
+};
+
+// The rows of a token's k slots (-1 for a slot without one) and its weights.
+// A row outside [0, n_rows) is an error of the caller's: recorded, and taken
+// as no row. A negative entry is a dropped slot.
+__device__ __forceinline__ void load_slots(const Args& a, int64_t t, int64_t* row, float* wt) {
+  if ((int)threadIdx.x < a.k) {
+    int64_t r = a.f2p[t * a.k + threadIdx.x];
+    if (r >= a.n_rows) {
+      if (atomicCAS(&a.status[0], 0, NVFP4MOE_ERR_INVALID) == 0) a.status[1] = 20;
+      r = -1;
+    }
+    row[threadIdx.x] = r;
+    wt[threadIdx.x] = a.w ? a.w[t * a.k + threadIdx.x] : 1.0f;
+  }
+  __syncthreads();
+}
+
+// Sums of KM values over the block in a fixed order; thread j < k writes slot j.
+template <int KM>
+__device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float (&dot)[KM], const int64_t* row) {
+  __shared__ float part[kThreads / 32][KM];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    float v = dot[j];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0) part[warp][j] = v;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < a.k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) s += part[i][threadIdx.x];
+    a.d_w[t * a.k + threadIdx.x] = row[threadIdx.x] >= 0 ? s : 0.0f;
+  }
+}
+
+// One token's row to its k rows. KM >= k slots are unrolled.
+template <typename T, int V, int KM, bool kDot>
+__global__ void __launch_bounds__(kThreads) spread_kernel(const Args a) {
+  __shared__ int64_t row[kMaxK];
+  __shared__ float wt[kMaxK];
+  const int64_t t = blockIdx.x;
+  load_slots(a, t, row, wt);
+  const T* src = static_cast<const T*>(a.token_in) + t * a.ldt_in;
+  float dot[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
+  const int64_t whole = a.K / V * V;
+  for (int64_t c = threadIdx.x * V; c < whole; c += kThreads * V) {
+    using P = Pack<T, V>;
+    const P x = *reinterpret_cast<const P*>(src + c);
+    P o[KM];
+    if constexpr (kDot) {
+#pragma unroll
+      for (int j = 0; j < KM; ++j)
+        if (j < a.k && row[j] >= 0)
+          o[j] = *reinterpret_cast<const P*>(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
+    }
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      if (j < a.k && row[j] >= 0) {
+        P y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float v = Elem<T>::get(x.e[i]);
+          y.e[i] = Elem<T>::put(wt[j] * v);
+          if constexpr (kDot) dot[j] = fmaf(v, Elem<T>::get(o[j].e[i]), dot[j]);
+        }
+        *reinterpret_cast<P*>(static_cast<T*>(a.rows_out) + row[j] * a.ldr_out + c) = y;
+      }
+    }
+  }
+  for (int64_t c = whole + threadIdx.x; c < a.K; c += kThreads) {   // the columns after the last whole pack
+    const float v = Elem<T>::get(src[c]);
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      if (j < a.k && row[j] >= 0) {
+        static_cast<T*>(a.rows_out)[row[j] * a.ldr_out + c] = Elem<T>::put(wt[j] * v);
+        if constexpr (kDot)
+          dot[j] = fmaf(v, Elem<T>::get(static_cast<const T*>(a.rows_in)[row[j] * a.ldr_in + c]), dot[j]);
+      }
+    }
+  }
+  if constexpr (kDot) store_dots<KM>(a, t, dot, row);
+}
+
+// The weighted sum of a token's k rows, in j order, rounded once.
+template <typename T, int V, int KM, bool kDot>
+__global__ void __launch_bounds__(kThreads) collect_kernel(const Args a) {
+  __shared__ int64_t row[kMaxK];
+  __shared__ float wt[kMaxK];
+  const int64_t t = blockIdx.x;
+  load_slots(a, t, row, wt);
+  const T* rows = static_cast<const T*>(a.rows_in);
+  const T* tok = kDot ? static_cast<const T*>(a.token_in) + t * a.ldt_in : nullptr;
+  T* out = static_cast<T*>(a.token_out) + t * a.ldt_out;
+  float dot[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
+  const int64_t whole = a.K / V * V;
+  for (int64_t c = threadIdx.x * V; c < whole; c += kThreads * V) {
+    using P = Pack<T, V>;
+    P r[KM], x;
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+      if (j < a.k && row[j] >= 0) r[j] = *reinterpret_cast<const P*>(rows + row[j] * a.ldr_in + c);
+    if constexpr (kDot) x = *reinterpret_cast<const P*>(tok + c);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      if (j < a.k && row[j] >= 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float v = Elem<T>::get(r[j].e[i]);
+          acc[i] = fmaf(wt[j], v, acc[i]);
+          if constexpr (kDot) dot[j] = fmaf(Elem<T>::get(x.e[i]), v, dot[j]);
+        }
+      }
+    }
+    P y;
+#pragma unroll
+    for (int i = 0; i < V; ++i) y.e[i] = Elem<T>::put(acc[i]);
+    *reinterpret_cast<P*>(out + c) = y;
+  }
+  for (int64_t c = whole + threadIdx.x; c < a.K; c += kThreads) {
+    float acc = 0.0f;
+    const float x = kDot ? Elem<T>::get(tok[c]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      if (j < a.k && row[j] >= 0) {
+        const float v = Elem<T>::get(rows[row[j] * a.ldr_in + c]);
+        acc = fmaf(wt[j], v, acc);
+        if constexpr (kDot) dot[j] = fmaf(x, v, dot[j]);
+      }
+    }
+    out[c] = Elem<T>::put(acc);
+  }
+  if constexpr (kDot) store_dots<KM>(a, t, dot, row);
+}
+
+template <typename T, int V, int KM>
+void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
+  const unsigned grid = (unsigned)a.T;
+  if (spread) {
+    if (dot) spread_kernel<T, V, KM, true><<<grid, kThreads, 0, s>>>(a);
+    else spread_kernel<T, V, KM, false><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    if (dot) collect_kernel<T, V, KM, true><<<grid, kThreads, 0, s>>>(a);
+    else collect_kernel<T, V, KM, false><<<grid, kThreads, 0, s>>>(a);
+  }
+}
+
+// 16-byte accesses where every row of every operand starts on a 16-byte
+// boundary, single elements otherwise.
+template <typename T>
+void launch_t(const Args& a, bool spread, bool dot, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  auto whole = [](const void* p, int64_t ld) { return !p || (aligned(p, 16) && ld * (int64_t)sizeof(T) % 16 == 0); };
+  const bool wide = whole(a.token_in, a.ldt_in) && whole(a.token_out, a.ldt_out) && whole(a.rows_in, a.ldr_in) &&
+                    whole(a.rows_out, a.ldr_out);
+  if (wide) {
+    if (a.k <= 4) launch_v<T, V, 4>(a, spread, dot, s);
+    else if (a.k <= 8) launch_v<T, V, 8>(a, spread, dot, s);
+    else launch_v<T, V, 16>(a, spread, dot, s);
+  } else {
+    if (a.k <= 4) launch_v<T, 1, 4>(a, spread, dot, s);
+    else if (a.k <= 8) launch_v<T, 1, 8>(a, spread, dot, s);
+    else launch_v<T, 1, 16>(a, spread, dot, s);
+  }
+}
+
+int launch(Args& a, int type, bool spread, bool dot, void* stream) {
+  a.status = device_status_word();
+  NVFP4_CHECK(a.status, NVFP4MOE_ERR_LAUNCH);
+  cudaStream_t s = as_stream(stream);
+  if (type == NVFP4MOE_BF16) launch_t<__nv_bfloat16>(a, spread, dot, s);
+  else if (type == NVFP4MOE_F16) launch_t<__half>(a, spread, dot, s);
+  else launch_t<float>(a, spread, dot, s);
+  return launch_status();
+}
+
+int check_sizes(int type, int64_t T, int64_t K, int k, int64_t n_rows) {
+  NVFP4_CHECK(type == NVFP4MOE_BF16 || type == NVFP4MOE_F16 || type == NVFP4MOE_F32, NVFP4MOE_ERR_UNSUPPORTED);
+  NVFP4_CHECK(T >= 0 && K >= 0 && k >= 1 && k <= kMaxK && n_rows >= 0 && T < (1ll << 31) && T * k < (1ll << 31),
+              NVFP4MOE_ERR_UNSUPPORTED);
+  return NVFP4MOE_OK;
+}
+
+bool element_aligned(const void* p, int type) { return aligned(p, type == NVFP4MOE_F32 ? 4 : 2); }
+
+int spread(const void* token, int64_t ldt, int type, int64_t T, int64_t K, int k, const int32_t* f2p,
+           const float* w, const void* dot_rows, int64_t ldd, void* rows, int64_t n_rows, int64_t ldr, float* d_w,
+           void* stream) {
+  NVFP4_TRY(check_sizes(type, T, K, k, n_rows));
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4_CHECK(f2p && (!dot_rows || (w && d_w)) && (dot_rows || !d_w), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(K == 0 || n_rows == 0 || (token && rows), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(ldt >= K && ldr >= K && (!dot_rows || ldd >= K), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(element_aligned(token, type) && element_aligned(rows, type) && element_aligned(dot_rows, type),
+              NVFP4MOE_ERR_INVALID);
+  if (K == 0 && !d_w) return NVFP4MOE_OK;
+  Args a{};
+  a.token_in = token; a.ldt_in = ldt;
+  a.rows_in = dot_rows; a.ldr_in = ldd;
+  a.rows_out = rows; a.ldr_out = ldr;
+  a.n_rows = n_rows; a.f2p = f2p; a.w = w; a.d_w = d_w; a.T = T; a.K = K; a.k = k;
+  return launch(a, type, true, d_w != nullptr, stream);
+}
+
+int collect(const void* rows, int64_t n_rows, int64_t ldr, int type, int64_t T, int64_t K, int k,
+            const int32_t* f2p, const float* w, const void* dot_token, int64_t ldd, void* token, int64_t ldt,
+            float* d_w, void* stream) {
+  NVFP4_TRY(check_sizes(type, T, K, k, n_rows));
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4_CHECK(f2p && (!dot_token || (w && d_w)) && (dot_token || !d_w), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(K == 0 || (token && (n_rows == 0 || rows)), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(ldt >= K && ldr >= K && (!dot_token || ldd >= K), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(element_aligned(token, type) && element_aligned(rows, type) && element_aligned(dot_token, type),
+              NVFP4MOE_ERR_INVALID);
+  if (K == 0 && !d_w) return NVFP4MOE_OK;
+  Args a{};
+  a.token_in = dot_token; a.ldt_in = ldd;
+  a.token_out = token; a.ldt_out = ldt;
+  a.rows_in = rows; a.ldr_in = ldr;
+  a.n_rows = n_rows; a.f2p = f2p; a.w = w; a.d_w = d_w; a.T = T; a.K = K; a.k = k;
+  return launch(a, type, false, d_w != nullptr, stream);
+}
+
+}  // namespace
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" int moe_sort_tokens(const void* x, int type, int64_t T, int64_t K, int64_t ldx,
+                               const int32_t* flat_to_perm, int k, const float* topk_w, void* rows, int64_t n_rows,
+                               int64_t ldr, void* stream) {
+  return spread(x, ldx, type, T, K, k, flat_to_perm, topk_w, nullptr, 0, rows, n_rows, ldr, nullptr, stream);
+}
+
+extern "C" int moe_sort_tokens_backward(const void* d_rows, int type, int64_t n_rows, int64_t K, int64_t ldr,
+                                        const int32_t* flat_to_perm, int64_t T, int k, const float* topk_w,
+                                        const void* x, int64_t ldx, void* dx, int64_t lddx, float* d_w,
+                                        void* stream) {
+  return collect(d_rows, n_rows, ldr, type, T, K, k, flat_to_perm, topk_w, x, ldx, dx, lddx, d_w, stream);
+}
+
+extern "C" int moe_unsort_tokens(const void* rows, int type, int64_t n_rows, int64_t K, int64_t ldr,
+                                 const int32_t* flat_to_perm, int64_t T, int k, const float* topk_w, void* y,
+                                 int64_t ldy, void* stream) {
+  return collect(rows, n_rows, ldr, type, T, K, k, flat_to_perm, topk_w, nullptr, 0, y, ldy, nullptr, stream);
+}
+
+extern "C" int moe_unsort_tokens_backward(const void* dy, int type, int64_t T, int64_t K, int64_t lddy,
+                                          const int32_t* flat_to_perm, int k, const float* topk_w, const void* rows,
+                                          int64_t ldr, void* d_rows, int64_t n_rows, int64_t lddr, float* d_w,
+                                          void* stream) {
+  return spread(dy, lddy, type, T, K, k, flat_to_perm, topk_w, rows, ldr, d_rows, n_rows, lddr, d_w, stream);
+}
