@@ -130,11 +130,18 @@ def lib():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# torch.cuda.current_stream() builds a Stream object (3 us of host time a call,
+# as much as the launch itself); the raw handle takes a tenth of one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(status, what):
@@ -405,83 +412,94 @@ def moe_combine(out, topk_w, flat_to_perm, y=None):
 # ------------------------------------------------------------------ tokens in expert order
 
 def _rows(t, name, types=_TYPES):
-    """A 2-D CUDA tensor of one of `types` whose rows are contiguous (any leading dimension)."""
+    """(rows, columns, leading dimension, address) of a 2-D CUDA tensor of one of
+    `types` whose rows are contiguous."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise NVFP4Error("%s must be a CUDA tensor" % name)
     if t.dtype not in types or t.dim() != 2:
         raise NVFP4Error("%s must be a matrix of one of %s" % (name, ", ".join(str(d) for d in types)))
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    n, c = t.shape
+    ld, step = t.stride()
+    if c > 1 and step != 1 or n > 1 and ld < c:
         raise NVFP4Error("the rows of %s must be contiguous and must not overlap" % name)
-    return t
-
-
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return n, c, ld if n > 1 else max(c, ld), t.data_ptr()
 
 
 def _flat(t, name, dtype, numel):
-    """A contiguous CUDA tensor of `numel` elements."""
+    """The address of a contiguous CUDA tensor of `numel` elements."""
     _dev(t, name)
     if t.dtype != dtype or t.numel() != numel:
         raise NVFP4Error("%s must have %d elements of %s" % (name, numel, dtype))
-    return t
+    return t.data_ptr()
 
 
-def _out(t, name, shape, dtype, device):
-    """The caller's output of that shape and type, or a new one."""
+def _out(t, name, n, c, like, dtype=None):
+    """The caller's (n, c) output, or a new one, with its leading dimension and address."""
+    dtype = dtype or like.dtype
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _rows(t, name, (dtype,))
-    if tuple(t.shape) != shape:
-        raise NVFP4Error("%s must be %s" % (name, "x".join(str(n) for n in shape)))
-    return t
+        t = torch.empty((n, c), dtype=dtype, device=like.device)
+        return t, c, t.data_ptr()
+    rows, cols, ld, ptr = _rows(t, name, (dtype,))
+    if rows != n or cols != c:
+        raise NVFP4Error("%s must be %dx%d" % (name, n, c))
+    return t, ld, ptr
 
 
 def _slots(flat_to_perm, k, topk_w):
+    """Tokens, and the addresses of flat_to_perm and topk_w."""
     _dev(flat_to_perm, "flat_to_perm")
     n = flat_to_perm.numel()
     if flat_to_perm.dtype != torch.int32 or k < 1 or n % k:
         raise NVFP4Error("flat_to_perm must be int32 with k entries a token")
-    if topk_w is not None:
-        _flat(topk_w, "topk_w", torch.float32, n)
-    return n // k
+    return n // k, flat_to_perm.data_ptr(), None if topk_w is None else _flat(topk_w, "topk_w", torch.float32, n)
+
+
+def _dots(t, name, n, c, like, topk_w, T, k):
+    """Leading dimension and address of the operand of the dot products, and the
+    (T, k) gradient of the weights with its address."""
+    if t is None:
+        return 0, None, None, None
+    rows, cols, ld, ptr = _rows(t, name, (like.dtype,))
+    if rows != n or cols != c or topk_w is None:
+        raise NVFP4Error("%s must be %dx%d, given together with topk_w" % (name, n, c))
+    d_w = torch.empty((T, k), dtype=torch.float32, device=like.device)
+    return ld, ptr, d_w, d_w.data_ptr()
 
 
 def moe_sort_tokens(x, flat_to_perm, k, topk_w=None, n_rows=None, rows=None):
     """x (T, K) in expert order: rows[flat_to_perm[t*k+j]] = topk_w[t, j] * x[t]
     (n_rows rows, T*k if not given; those that no entry names are not written)."""
-    _rows(x, "x")
-    T, K = x.shape
-    if _slots(flat_to_perm, k, topk_w) != T:
+    T, K, ldx, px = _rows(x, "x")
+    tokens, pf, pw = _slots(flat_to_perm, k, topk_w)
+    if tokens != T:
         raise NVFP4Error("flat_to_perm must have k entries for each row of x")
-    rows = _out(rows, "rows", (rows.shape[0] if rows is not None and n_rows is None else
-                               T * k if n_rows is None else n_rows, K), x.dtype, x.device)
-    _check(lib().moe_sort_tokens(_ptr(x), _TYPES[x.dtype], T, K, _ld(x), _ptr(flat_to_perm), k, _ptr(topk_w),
-                                 _ptr(rows), rows.shape[0], _ld(rows), _stream()), "moe_sort_tokens")
+    if n_rows is None:
+        n_rows = T * k if rows is None else rows.shape[0]
+    rows, ldr, pr = _out(rows, "rows", n_rows, K, x)
+    _check(lib().moe_sort_tokens(px, _TYPES[x.dtype], T, K, ldx, pf, k, pw, pr, n_rows, ldr, _stream()),
+           "moe_sort_tokens")
     return rows
 
 
 def moe_sort_tokens_backward(d_rows, flat_to_perm, k, topk_w=None, x=None, dx=None):
     """The gradients of moe_sort_tokens: (dx, d_w); d_w is computed when x (and
     topk_w) is given, else None."""
-    _rows(d_rows, "d_rows")
-    T, K = _slots(flat_to_perm, k, topk_w), d_rows.shape[1]
-    d_w = _dots(x, "x", (T, K), d_rows, topk_w, T, k)
-    dx = _out(dx, "dx", (T, K), d_rows.dtype, d_rows.device)
-    _check(lib().moe_sort_tokens_backward(_ptr(d_rows), _TYPES[d_rows.dtype], d_rows.shape[0], K, _ld(d_rows),
-                                          _ptr(flat_to_perm), T, k, _ptr(topk_w), _ptr(x),
-                                          0 if x is None else _ld(x), _ptr(dx), _ld(dx), _ptr(d_w), _stream()),
-           "moe_sort_tokens_backward")
+    n_rows, K, ldr, pr = _rows(d_rows, "d_rows")
+    T, pf, pw = _slots(flat_to_perm, k, topk_w)
+    ldx, px, d_w, pd = _dots(x, "x", T, K, d_rows, topk_w, T, k)
+    dx, lddx, po = _out(dx, "dx", T, K, d_rows)
+    _check(lib().moe_sort_tokens_backward(pr, _TYPES[d_rows.dtype], n_rows, K, ldr, pf, T, k, pw, px, ldx, po, lddx,
+                                          pd, _stream()), "moe_sort_tokens_backward")
     return dx, d_w
 
 
 def moe_unsort_tokens(rows, flat_to_perm, k, topk_w=None, y=None):
     """y[t] = sum_j topk_w[t, j] * rows[flat_to_perm[t*k+j]]."""
-    _rows(rows, "rows")
-    T, K = _slots(flat_to_perm, k, topk_w), rows.shape[1]
-    y = _out(y, "y", (T, K), rows.dtype, rows.device)
-    _check(lib().moe_unsort_tokens(_ptr(rows), _TYPES[rows.dtype], rows.shape[0], K, _ld(rows), _ptr(flat_to_perm),
-                                   T, k, _ptr(topk_w), _ptr(y), _ld(y), _stream()), "moe_unsort_tokens")
+    n_rows, K, ldr, pr = _rows(rows, "rows")
+    T, pf, pw = _slots(flat_to_perm, k, topk_w)
+    y, ldy, py = _out(y, "y", T, K, rows)
+    _check(lib().moe_unsort_tokens(pr, _TYPES[rows.dtype], n_rows, K, ldr, pf, T, k, pw, py, ldy, _stream()),
+           "moe_unsort_tokens")
     return y
 
 
@@ -489,29 +507,17 @@ def moe_unsort_tokens_backward(dy, flat_to_perm, k, topk_w=None, rows=None, n_ro
     """The gradients of moe_unsort_tokens: (d_rows, d_w); d_w is computed when
     rows (and topk_w) is given, else None. Rows that no entry of flat_to_perm
     names are not written."""
-    _rows(dy, "dy")
-    T, K = dy.shape
-    if _slots(flat_to_perm, k, topk_w) != T:
+    T, K, ldy, py = _rows(dy, "dy")
+    tokens, pf, pw = _slots(flat_to_perm, k, topk_w)
+    if tokens != T:
         raise NVFP4Error("flat_to_perm must have k entries for each row of dy")
     if n_rows is None:
         n_rows = rows.shape[0] if rows is not None else d_rows.shape[0] if d_rows is not None else T * k
-    d_w = _dots(rows, "rows", (n_rows, K), dy, topk_w, T, k)
-    d_rows = _out(d_rows, "d_rows", (n_rows, K), dy.dtype, dy.device)
-    _check(lib().moe_unsort_tokens_backward(_ptr(dy), _TYPES[dy.dtype], T, K, _ld(dy), _ptr(flat_to_perm), k,
-                                            _ptr(topk_w), _ptr(rows), 0 if rows is None else _ld(rows),
-                                            _ptr(d_rows), n_rows, _ld(d_rows), _ptr(d_w), _stream()),
-           "moe_unsort_tokens_backward")
+    ldr, pr, d_w, pd = _dots(rows, "rows", n_rows, K, dy, topk_w, T, k)
+    d_rows, lddr, po = _out(d_rows, "d_rows", n_rows, K, dy)
+    _check(lib().moe_unsort_tokens_backward(py, _TYPES[dy.dtype], T, K, ldy, pf, k, pw, pr, ldr, po, n_rows, lddr, pd,
+                                            _stream()), "moe_unsort_tokens_backward")
     return d_rows, d_w
-
-
-def _dots(t, name, shape, like, topk_w, T, k):
-    """The (T, k) gradient of the weights if the operand of its dot products is given."""
-    if t is None:
-        return None
-    _rows(t, name, (like.dtype,))
-    if tuple(t.shape) != shape or topk_w is None:
-        raise NVFP4Error("%s must be %dx%d, given together with topk_w" % (name, *shape))
-    return torch.empty((T, k), dtype=torch.float32, device=like.device)
 
 
 # ------------------------------------------------------------------ 8-bit block-scaled operands
@@ -520,38 +526,45 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _codes_and_scales(codes, sf, n, K, device):
+    """The caller's codes and scales of n rows, or new ones, with their addresses."""
+    kb = _blocks(K)
+    if codes is None:
+        codes = torch.empty((n, K), dtype=torch.uint8, device=device)
+    else:
+        _flat(codes, "codes", torch.uint8, n * K)
+    if sf is None:
+        sf = torch.empty((n, kb), dtype=torch.float32, device=device)
+    else:
+        _flat(sf, "sf", torch.float32, n * kb)
+    return codes, sf, codes.data_ptr(), sf.data_ptr()
+
+
 def fp8_quantize(x, flat_to_perm=None, k=1, out_rows=None, codes=None, sf=None):
     """(rows, K) BF16, F16 or F32 -> E4M3 codes (uint8) and one f32 scale per row
     and 128 elements. With flat_to_perm, row r is written to the k rows
     flat_to_perm[r*k .. r*k+k) of the out_rows (rows*k if not given) output rows."""
-    _rows(x, "x")
-    M, K = x.shape
-    if flat_to_perm is not None and _slots(flat_to_perm, k, None) != M:
-        raise NVFP4Error("flat_to_perm must have k entries for each row of x")
+    M, K, ldx, px = _rows(x, "x")
+    pf = None
+    if flat_to_perm is not None:
+        n, pf, _ = _slots(flat_to_perm, k, None)
+        if n != M:
+            raise NVFP4Error("flat_to_perm must have k entries for each row of x")
     if out_rows is None:
         out_rows = M if flat_to_perm is None else M * k
-    codes = torch.empty((out_rows, K), dtype=torch.uint8, device=x.device) if codes is None else \
-        _flat(codes, "codes", torch.uint8, out_rows * K)
-    sf = torch.empty((out_rows, _blocks(K)), dtype=torch.float32, device=x.device) if sf is None else \
-        _flat(sf, "sf", torch.float32, out_rows * _blocks(K))
-    _check(lib().fp8_quantize(_ptr(x), _TYPES[x.dtype], M, K, _ld(x), _ptr(flat_to_perm), k, out_rows, _ptr(codes),
-                              _ptr(sf), _stream()), "fp8_quantize")
+    codes, sf, pc, ps = _codes_and_scales(codes, sf, out_rows, K, x.device)
+    _check(lib().fp8_quantize(px, _TYPES[x.dtype], M, K, ldx, pf, k, out_rows, pc, ps, _stream()), "fp8_quantize")
     return codes, sf
 
 
 def fp8_swiglu_quantize(gate_up, codes=None, sf=None):
     """Rows [gate | up] (rows, 2I) -> codes and scales of silu(gate) * up."""
-    _rows(gate_up, "gate_up")
-    M, two_i = gate_up.shape
+    M, two_i, ld, px = _rows(gate_up, "gate_up")
     if two_i % 2:
         raise NVFP4Error("gate_up must have as many up as gate columns")
-    I = two_i // 2
-    codes = torch.empty((M, I), dtype=torch.uint8, device=gate_up.device) if codes is None else \
-        _flat(codes, "codes", torch.uint8, M * I)
-    sf = torch.empty((M, _blocks(I)), dtype=torch.float32, device=gate_up.device) if sf is None else \
-        _flat(sf, "sf", torch.float32, M * _blocks(I))
-    _check(lib().fp8_swiglu_quantize(_ptr(gate_up), _TYPES[gate_up.dtype], M, I, _ld(gate_up), _ptr(codes), _ptr(sf),
-                                     _stream()), "fp8_swiglu_quantize")
+    codes, sf, pc, ps = _codes_and_scales(codes, sf, M, two_i // 2, gate_up.device)
+    _check(lib().fp8_swiglu_quantize(px, _TYPES[gate_up.dtype], M, two_i // 2, ld, pc, ps, _stream()),
+           "fp8_swiglu_quantize")
     return codes, sf
 
 
@@ -572,47 +585,43 @@ def fp8_quantize_weight(w):
 def fp8_linear(a_codes, a_sf, w_codes, w_sf, out=None, out_dtype=torch.bfloat16):
     """A (M, K) x W (N, K) -> C (M, N): codes uint8 or float8_e4m3fn, scales f32
     as fp8_quantize and fp8_quantize_weight give them."""
-    _rows(a_codes, "a_codes", _CODES)
-    _rows(w_codes, "w_codes", _CODES)
-    M, K = a_codes.shape
-    N = w_codes.shape[0]
-    if w_codes.shape[1] != K:
+    M, K, lda, pa = _rows(a_codes, "a_codes", _CODES)
+    N, wk, ldw, pw = _rows(w_codes, "w_codes", _CODES)
+    if wk != K:
         raise NVFP4Error("a_codes and w_codes must have the same K")
-    _flat(a_sf, "a_sf", torch.float32, M * _blocks(K))
-    _flat(w_sf, "w_sf", torch.float32, _blocks(N) * _blocks(K))
-    out = _c_out(out, M, N, out_dtype, a_codes.device)
-    _check(lib().fp8_linear(_ptr(a_codes), _ptr(a_sf), M, _ld(a_codes), _ptr(w_codes), _ptr(w_sf), N, K,
-                            _ld(w_codes), _ptr(out), _TYPES[out.dtype], _ld(out), _stream()), "fp8_linear")
+    kb = _blocks(K)
+    psa = _flat(a_sf, "a_sf", torch.float32, M * kb)
+    psw = _flat(w_sf, "w_sf", torch.float32, _blocks(N) * kb)
+    dtype, out_type = _c_type(out, out_dtype)
+    out, ldc, pc = _out(out, "out", M, N, a_codes, dtype)
+    _check(lib().fp8_linear(pa, psa, M, lda, pw, psw, N, K, ldw, pc, out_type, ldc, _stream()), "fp8_linear")
     return out
 
 
 def fp8_grouped_gemm(a_codes, a_sf, w_codes, w_sf, offsets, out=None, out_dtype=torch.bfloat16):
     """A (M, K), rows grouped by expert (compact rows, offsets (E + 1) int32), x
     W (E, N, K) -> C (M, N)."""
-    _rows(a_codes, "a_codes", _CODES)
+    M, K, lda, pa = _rows(a_codes, "a_codes", _CODES)
     _dev(w_codes, "w_codes")
-    if w_codes.dtype not in _CODES or w_codes.dim() != 3:
-        raise NVFP4Error("w_codes must be (E, N, K) codes")
-    M, K = a_codes.shape
+    if w_codes.dtype not in _CODES or w_codes.dim() != 3 or w_codes.shape[2] != K:
+        raise NVFP4Error("w_codes must be (E, N, K) codes with the K of a_codes")
     E, N = w_codes.shape[:2]
-    if w_codes.shape[2] != K:
-        raise NVFP4Error("a_codes and w_codes must have the same K")
-    _flat(a_sf, "a_sf", torch.float32, M * _blocks(K))
-    _flat(w_sf, "w_sf", torch.float32, E * _blocks(N) * _blocks(K))
-    _flat(offsets, "offsets", torch.int32, E + 1)
-    out = _c_out(out, M, N, out_dtype, a_codes.device)
-    _check(lib().fp8_grouped_gemm(_ptr(a_codes), _ptr(a_sf), M, _ld(a_codes), _ptr(w_codes), _ptr(w_sf),
-                                  _ptr(offsets), E, N, K, K, _ptr(out), _TYPES[out.dtype], _ld(out), _stream()),
-           "fp8_grouped_gemm")
+    kb = _blocks(K)
+    psa = _flat(a_sf, "a_sf", torch.float32, M * kb)
+    psw = _flat(w_sf, "w_sf", torch.float32, E * _blocks(N) * kb)
+    po = _flat(offsets, "offsets", torch.int32, E + 1)
+    dtype, out_type = _c_type(out, out_dtype)
+    out, ldc, pc = _out(out, "out", M, N, a_codes, dtype)
+    _check(lib().fp8_grouped_gemm(pa, psa, M, lda, w_codes.data_ptr(), psw, po, E, N, K, K, pc, out_type, ldc,
+                                  _stream()), "fp8_grouped_gemm")
     return out
 
 
-def _c_out(out, M, N, dtype, device):
-    if out is None:
-        if dtype not in _TYPES:
-            raise NVFP4Error("out_dtype must be one of %s" % ", ".join(str(d) for d in _TYPES))
-        return torch.empty((M, N), dtype=dtype, device=device)
-    return _out(out, "out", (M, N), out.dtype if out.dtype in _TYPES else dtype, device)
+def _c_type(out, out_dtype):
+    dtype = out_dtype if out is None else out.dtype
+    if dtype not in _TYPES:
+        raise NVFP4Error("the result must be one of %s" % ", ".join(str(d) for d in _TYPES))
+    return dtype, _TYPES[dtype]
 
 
 # ------------------------------------------------------------------ the forward

@@ -546,12 +546,16 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
                                              uint64_t limit_ns, int* status, int site, uint32_t peer_abort = 0) {
   auto probe = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
   if (probe()) return true;
-  const uint64_t t0 = global_timer_ns();
+  // the clock is read only now and then: a read of it on every wait that does
+  // not succeed at once would sit on the path of each hand-off between warps
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (probe()) return true;
     if ((it & 15u) == 0) {
       if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
         *abort_flag = 1;
         if (peer_abort) st_shared_cluster_u32(peer_abort, 1u);
         if (atomicCAS(&status[0], 0, NVFP4MOE_ERR_DEVICE_TIMEOUT) == 0) status[1] = site;

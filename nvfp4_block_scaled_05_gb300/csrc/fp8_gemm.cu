@@ -12,10 +12,12 @@
 //
 // Tile: 128 activation rows of one group x 256 weight rows; a stage is one
 // block of K, 128 bytes of every operand row (one 128-byte swizzle row).
-// Warp roles (320 threads, one CTA per SM):
-//   warp 0     TMA producer, a ring of 4 stages of 48 KB
-//   warp 1     TMEM owner; one lane issues the MMAs
-//   warps 2-9  epilogue, two warps per TMEM lane quadrant (128 columns each)
+// Warp roles (384 threads, one CTA per SM):
+//   warp 0      TMA producer, a ring of 4 stages of 48 KB
+//   warp 1      TMEM owner; issues the MMAs
+//   warps 2-3   the factors sa * sw of every row and block, into a ring in
+//               shared memory
+//   warps 4-11  epilogue, two warps per TMEM lane quadrant (128 columns each)
 // Tiles are ordered group-major, then weight tile, then activation tile, so
 // the activation tiles that share a weight tile run at the same time and it
 // leaves HBM once.
@@ -28,6 +30,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 namespace nvfp4moe {
 namespace {
 
@@ -35,16 +39,24 @@ constexpr int BM = 128;
 constexpr int BN = 256;
 constexpr int BK = 128;                  // K elements (bytes) per stage: one scale block
 constexpr int STAGES = 4;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int HN = BN / 2;               // columns of one epilogue warpgroup
+constexpr int kEpiWarp0 = 4;             // the first of two epilogue warpgroups
+constexpr int kThreads = 32 * (kEpiWarp0 + 8);
 constexpr int A_BYTES = BM * BK;         // 16 KB
 constexpr int B_BYTES = BN * BK;         // 32 KB
 constexpr int OFF_B = STAGES * A_BYTES;
 constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
-constexpr int OFF_MISC = OFF_BAR + 256;
+constexpr int kScaleBlocks = 4;          // blocks of K whose scales change hands together
+constexpr int kScaleSlots = 4;           // such groups on their way
+constexpr int SCALE_FLOATS = 2 * kScaleBlocks * BM;   // of one group: [half][block][row]
+constexpr int OFF_SCALE = OFF_BAR + 256;
+constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * SCALE_FLOATS * 4;
 constexpr int OFF_SCHED = OFF_MISC + 64;
-constexpr uint32_t TMEM_COLS = 512;      // two accumulator buffers of 256 columns
+constexpr uint32_t TMEM_COLS = 512;      // two buffers of 256 columns
+constexpr int kPartBytes = BN * 4 + 16;  // a row of partial sums in shared memory; 16 bytes against bank conflicts
+constexpr int kMaxSplit = 8;
 constexpr int kMaxGroups = 1024;
+static_assert(BM * kPartBytes <= OFF_BAR, "the partial sums lie in the ring");
 
 struct Params {
   const float* a_sf;          // (M, KB)
@@ -55,19 +67,20 @@ struct Params {
   void* c;
   int c_type;
   int64_t ldc;
+  int w_once;                 // few rows: every weight row is read by one tile only
+  int split;                  // CTAs (a cluster) that share a tile's blocks of K
   int c_32B;                  // c and ldc allow 32-byte stores
   uint64_t wait_limit_ns;
   int* status;
   int test_stall;             // test hook: the MMA issuer first waits on a barrier nobody arrives on
 };
 
-// First row of every group (start[E] = the end of the last) and first tile of
-// every group. Bounds outside [0, M] or out of order are clamped, so that no
-// tile reaches past the operands whatever the offsets hold.
+// Tiles of tm activation rows of one group x tn weight rows, ordered
+// group-major, then weight tile, then activation tile.
 struct Sched {
-  const int32_t* start;       // [2E]: first row, rows
-  const int32_t* tile_start;  // [E + 1]
-  int E, NT, N;
+  const int32_t* start;       // [2E]: first row and rows of every group
+  const int32_t* tile_start;  // [E + 1]: first tile of every group
+  int E, NT, N, tm, tn;
   __device__ __forceinline__ void decode(int t, int& e, int& nb, int& row0, int& rows, int& ncols) const {
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // largest e with tile_start[e] <= t
@@ -80,17 +93,58 @@ struct Sched {
     const int local = t - tile_start[e];
     nb = local / mt;
     const int mb = local - nb * mt;
-    row0 = start[2 * e] + mb * BM;
-    rows = min(BM, start[2 * e + 1] - mb * BM);
-    ncols = min(BN, N - nb * BN);
+    row0 = start[2 * e] + mb * tm;
+    rows = min(tm, start[2 * e + 1] - mb * tm);
+    ncols = min(tn, N - nb * tn);
   }
 };
+
+// The rows of every group, by all threads. Bounds outside [0, M] or out of
+// order are clamped, so that no tile reaches past the operands whatever the
+// offsets hold.
+__device__ __forceinline__ void load_groups(const Params& p, int32_t* start) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int lo = 0, hi = p.M;
+    if (p.offsets) {
+      lo = min(max(p.offsets[e], 0), p.M);
+      hi = min(max(p.offsets[e + 1], lo), p.M);
+    }
+    start[2 * e] = lo;
+    start[2 * e + 1] = hi - lo;
+  }
+}
+
+// The prefix sum of the groups' tiles, by one warp.
+__device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* tile_start) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = 0; base < sch.E; base += 32) {
+    const int e = base + lane;
+    const int mt = e < sch.E ? (sch.start[2 * e + 1] + sch.tm - 1) / sch.tm : 0;
+    int incl = mt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (e < sch.E) tile_start[e] = (carry + incl - mt) * sch.NT;
+    carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  if (lane == 0) tile_start[sch.E] = carry * sch.NT;
+}
 
 // Instruction descriptor: kind::f8f6f4, A and B E4M3 K-major, f32 accumulate.
 __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4)                                  // D format: f32
          | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -102,18 +156,24 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t b
       : "memory");
 }
 
-// 32 consecutive columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tc_ld32_wait(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 consecutive columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tc_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// Four f32 of another CTA's shared memory (shared::cluster address).
+__device__ __forceinline__ void ld_shared_cluster_v4(uint32_t addr, float* v) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float a, float b) {
@@ -152,11 +212,65 @@ __device__ __forceinline__ void store16(T* out, const float* v, int n, bool wide
   }
 }
 
+// The first n of 8 values to out: 16-byte stores where the rows allow them.
 template <typename T>
-__device__ __forceinline__ void store_row(T* out, const float (&acc)[128], int n, bool wide) {
+__device__ __forceinline__ void store8(T* out, const float (&v)[8], int n, bool wide) {
+  if (wide && n >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4*>(out) = make_uint4(pack2(out, v[0], v[1]), pack2(out, v[2], v[3]),
+                                                  pack2(out, v[4], v[5]), pack2(out, v[6], v[7]));
+    } else {
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+    for (int i = 0; i < 8; ++i)
+      if (i < n) put(out + i, v[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* out, const float (&acc)[HN], int n, bool wide) {
+#pragma unroll
+  for (int j = 0; j < HN / 16; ++j)
     if (16 * j < n) store16(out + 16 * j, acc + 16 * j, n - 16 * j, wide);
+}
+
+// C's rows [row0, row0 + rows), columns [col0, col0 + ncols) from the partial
+// sums of `split` CTAs (rows of TN f32, part_bytes apart, at the same place in
+// the shared memory of each): eight columns of a row by one thread, added in
+// the order of the blocks of K.
+template <int TN>
+__device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int part_bytes, int rank, int split,
+                                           int row0, int rows, int col0, int ncols, int threads) {
+  for (int i = rank * threads + threadIdx.x; i < rows * (TN / 8); i += split * threads) {
+    const int row = i / (TN / 8), col = i % (TN / 8) * 8;
+    if (col >= ncols) continue;
+    // all parts are on their way at once: a remote load takes about a microsecond
+    float w[kMaxSplit][8], v[8];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {
+      if (r < split) {
+        const uint32_t own = sbase + row * part_bytes + col * 4;
+        const uint32_t from = split > 1 ? mapa_shared(own, r) : own;
+        ld_shared_cluster_v4(from, w[r]);
+        ld_shared_cluster_v4(from + 16, w[r] + 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = w[0][k];
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r)
+        if (r < split) v[k] += w[r][k];
+    }
+    const int64_t at = (int64_t)(row0 + row) * p.ldc + col0 + col;
+    const int n = min(8, ncols - col);
+    if (p.c_type == NVFP4MOE_BF16) store8(static_cast<__nv_bfloat16*>(p.c) + at, v, n, p.c_32B);
+    else if (p.c_type == NVFP4MOE_F16) store8(static_cast<__half*>(p.c) + at, v, n, p.c_32B);
+    else store8(static_cast<float*>(p.c) + at, v, n, p.c_32B);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -170,35 +284,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bar_full = sbase + OFF_BAR;            // STAGES: a stage's tiles landed
-  const uint32_t bar_empty = bar_full + STAGES * 8;     // STAGES: its MMAs are done
-  const uint32_t bar_accf = bar_empty + STAGES * 8;     // 2: a buffer holds a block's products
-  const uint32_t bar_acce = bar_accf + 16;              // 2: the epilogue has read it
-  const uint32_t bar_aux = bar_acce + 16;               // MMA drain on abort
+  // STAGES: the stage's MMAs are done. The epilogue waits for it before it
+  // reads the products, the producer before it fills the stage again: one
+  // commit a block serves both. It cannot complete again before the epilogue
+  // has seen it: that takes the MMAs of STAGES blocks later, which wait for
+  // the epilogue's release of a buffer that it gives only after this block.
+  const uint32_t bar_done = bar_full + STAGES * 8;
+  const uint32_t bar_acce = bar_done + STAGES * 8;      // 2: the epilogue has read buffer b, columns 256 b on
+  const uint32_t bar_sff = bar_acce + 16;               // kScaleSlots: a group of scales is in shared memory
+  const uint32_t bar_sfe = bar_sff + kScaleSlots * 8;   // kScaleSlots: the epilogue has read it
+  const uint32_t bar_aux = bar_sfe + kScaleSlots * 8;   // MMA drain on abort
   const uint32_t bar_never = bar_aux + 8;               // never arrived on (failure-path test)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  float* scales = reinterpret_cast<float*>(smem + OFF_SCALE);
   int32_t* start = reinterpret_cast<int32_t*>(smem + OFF_SCHED);
   int32_t* tile_start = start + 2 * p.E;
   const int E = p.E, NT = (p.N + BN - 1) / BN;
 
-  // --- schedule: rows of every group, then the prefix sum of its tiles
-  for (int e = tid; e < E; e += kThreads) {
-    int lo = 0, hi = p.M;
-    if (p.offsets) {
-      lo = min(max(p.offsets[e], 0), p.M);
-      hi = min(max(p.offsets[e + 1], lo), p.M);
-    }
-    start[2 * e] = lo;
-    start[2 * e + 1] = hi - lo;
-  }
+  load_groups(p, start);
   if (tid == 32) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_done + 8 * s, 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar_accf + 8 * b, 1);
-      mbar_init(bar_acce + 8 * b, kEpiWarps);
+    for (int b = 0; b < 2; ++b) mbar_init(bar_acce + 8 * b, 8);
+    for (int b = 0; b < kScaleSlots; ++b) {
+      mbar_init(bar_sff + 8 * b, 64);
+      mbar_init(bar_sfe + 8 * b, 8);
     }
     mbar_init(bar_aux, 1);
     mbar_init(bar_never, 1);
@@ -210,29 +323,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int base = 0; base < E; base += 32) {
-      const int e = base + lane;
-      const int mt = e < E ? (start[2 * e + 1] + BM - 1) / BM : 0;
-      int incl = mt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += y;
-      }
-      if (e < E) tile_start[e] = (carry + incl - mt) * NT;
-      carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    if (lane == 0) tile_start[E] = carry * NT;
-  }
+  const Sched sch{start, tile_start, E, NT, p.N, BM, BN};
+  if (warp == 0) scan_tiles(sch, tile_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = tile_start[E];
-  const Sched sch{start, tile_start, E, NT, p.N};
   const int KB = p.KB;
+  // One CTA takes whole tiles in turn; a cluster of `split` takes one tile,
+  // each CTA a range of the blocks of K.
+  const int split = p.split;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / split, stride = (int)gridDim.x / split;
+  const int kb0 = KB * rank / split, kb1 = KB * (rank + 1) / split;
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- producer
@@ -243,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol_a = l2_policy_evict_last();
     uint32_t stage = 0, phase = 0, filled = 0, fill_phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
       sch.decode(t, e, nb, row0, rows, ncols);
       const CUtensorMap* tma = rows <= 16 ? &tm_a16 : rows <= 32 ? &tm_a32 : rows <= 64 ? &tm_a64 : &tm_a128;
@@ -254,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tx = (uint32_t)(box * BK + (ncols <= 128 ? 128 : 256) * BK);
       const int b_row = e * p.N + nb * BN;
       const uint64_t pol_w = tile_start[e + 1] - tile_start[e] > NT ? pol_wn : pol_w1;
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!wait_bounded(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 31)) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bounded(bar_done + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 31)) {
           ok = false;
           break;
         }
@@ -274,94 +378,179 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok)   // copies still in flight complete before the CTA may exit
       for (int s = 0; s < STAGES; ++s)
         if ((filled >> s) & 1u) drain_wait(bar_full + 8 * s, (fill_phase >> s) & 1u);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
+    // The whole warp runs the loop and one elected lane issues, so that the
+    // descriptors stay in uniform registers.
+    const bool leader = elect_one();
     uint32_t stage = 0, phase = 0, g = 0;
     bool ok = true, issued = false;
     const uint64_t adesc0 = sdesc_kmajor_sw128(sbase);
     const uint64_t bdesc0 = sdesc_kmajor_sw128(sbase + OFF_B);
-    if (p.test_stall && (int)blockIdx.x < total)
-      ok = wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 32);
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    if (p.test_stall && first < total)
+      ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 32));
+    for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
       sch.decode(t, e, nb, row0, rows, ncols);
       const uint32_t idesc = idesc_e4m3(BM, (ncols + 15) / 16 * 16);
-      for (int kb = 0; kb < KB; ++kb, ++g) {
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t buf = g & 1u;
-        if (!wait_bounded(bar_acce + 8 * buf, ((g >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 33) ||
-            !wait_bounded(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 34)) {
-          ok = false;
-          break;
-        }
+        ok = wait_bounded(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 34) &&
+             wait_bounded(bar_acce + 8 * buf, ((g >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 33);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ad = adesc0 + ((stage * A_BYTES) >> 4);
         const uint64_t bd = bdesc0 + ((stage * B_BYTES) >> 4);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk)   // 32 bytes of every row further per step
-          tc_mma_f8(tmem + buf * BN, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+          for (int kk = 0; kk < BK / 32; ++kk)   // 32 bytes of every row further per step
+            tc_mma_f8(tmem + buf * BN, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+          tc_commit(bar_done + 8 * stage);
+        }
         issued = true;
-        tc_commit(bar_empty + 8 * stage);
-        tc_commit(bar_accf + 8 * buf);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    if (!ok && issued) {   // tensor-core work in flight completes before the tensor memory is freed
+    if (!ok && issued && leader) {   // tensor-core work in flight completes before the tensor memory is freed
       tc_commit(bar_aux);
       drain_wait(bar_aux, 0);
     }
-  } else if (warp >= 2) {
-    // ---------------------------------------------------------------- epilogue
-    const int quad = warp & 3;              // TMEM lane quadrant this warp may access
-    const int half = (warp - 2) >> 2;       // columns [128 * half, 128 * half + 128): one weight scale a block
-    const int row = quad * 32 + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-    uint32_t g = 0;
+  } else if (warp == 2 || warp == 3) {
+    // ---------------------------------------------------------------- scales
+    // Thread i makes the factors of rows i and i + 64, for both column halves
+    // (a weight block each), four blocks of K at a time and up to four such
+    // groups ahead. The epilogue then reads one word a block: with the loads
+    // in the epilogue, every block waited for them (linear 4096 x 4096 x 7168:
+    // 147 us against 114 with a constant in their place).
+    const int i = tid - 64;
+    uint32_t slot = 0, phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
       sch.decode(t, e, nb, row0, rows, ncols);
-      const bool live = quad * 32 < rows && half * 128 < ncols;   // the whole warp
-      const bool active = row < rows && half * 128 < ncols;
-      const int64_t m = row0 + min(row, rows - 1);
-      const float* sa = p.a_sf + m * KB;
-      const float* sw = p.w_sf + ((int64_t)e * p.NB + min(nb * 2 + half, p.NB - 1)) * KB;
-      float acc[128];
+      const float* sa = p.a_sf + (int64_t)row0 * KB;
+      const float* sw0 = p.w_sf + ((int64_t)e * p.NB + nb * 2) * KB;
+      const float* sw1 = ncols > HN ? sw0 + KB : sw0;
+      for (int kg = kb0; kg < kb1; kg += kScaleBlocks) {
+        float a[2][kScaleBlocks], w0[kScaleBlocks], w1[kScaleBlocks];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      float s = live ? sa[0] * sw[0] : 0.0f;
-      for (int kb = 0; kb < KB; ++kb, ++g) {
-        const float s_next = live && kb + 1 < KB ? sa[kb + 1] * sw[kb + 1] : 0.0f;
+        for (int k = 0; k < kScaleBlocks; ++k) {
+          const bool in = kg + k < kb1;
+          w0[k] = in ? __ldg(sw0 + kg + k) : 0.0f;
+          w1[k] = in ? __ldg(sw1 + kg + k) : 0.0f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            a[h][k] = in && i + 64 * h < rows ? __ldg(sa + (int64_t)(i + 64 * h) * KB + kg + k) : 0.0f;
+        }
+        if (!wait_bounded(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 36)) {
+          ok = false;
+          break;
+        }
+        float* out = scales + slot * SCALE_FLOATS + i;
+#pragma unroll
+        for (int k = 0; k < kScaleBlocks; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            out[k * BM + 64 * h] = a[h][k] * w0[k];
+            out[(kScaleBlocks + k) * BM + 64 * h] = a[h][k] * w1[k];
+          }
+        mbar_arrive(bar_sff + 8 * slot);
+        if (++slot == kScaleSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ---------------------------------------------------------------- epilogue
+    const int quad = warp & 3;              // TMEM lane quadrant this warp may access
+    const int half = (warp - kEpiWarp0) >> 2;
+    const int col0 = half * HN;             // its columns are those of one 128-wide weight block
+    const int row = quad * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
+    uint32_t g = 0, stage = 0, phase = 0, slot = 0, sphase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < total; t += stride) {
+      int e, nb, row0, rows, ncols;
+      sch.decode(t, e, nb, row0, rows, ncols);
+      const bool live = quad * 32 < rows && col0 < ncols;   // the whole warp
+      const bool active = row < rows && col0 < ncols;
+      const int64_t m = row0 + min(row, rows - 1);
+      float acc[HN];
+#pragma unroll
+      for (int i = 0; i < HN; ++i) acc[i] = 0.0f;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t buf = g & 1u;
-        ok = wait_bounded(bar_accf + 8 * buf, (g >> 1) & 1u, abort_flag, p.wait_limit_ns, p.status, 35);
+        const int in_group = (kb - kb0) % kScaleBlocks;
+        if (in_group == 0)
+          ok = wait_bounded(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 37);
+        const float s = scales[slot * SCALE_FLOATS + (half * kScaleBlocks + in_group) * BM + row];
+        ok = ok && wait_bounded(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 35);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
         if (live) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tc_ld32_wait(taddr + buf * BN + 32 * c, v);
+          for (int c = 0; c < HN / 16; ++c) {
+            uint32_t v[16];
+            tc_ld16_wait(taddr + buf * BN + 16 * c, v);
+            if (c + 1 == HN / 16) {   // all read: released before the last are added
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * c + i]);
+            for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[16 * c + i]);
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
+        }
+        if (in_group == kScaleBlocks - 1 || kb + 1 == kb1) {
+          __syncwarp();   // every lane has used its scale of the group's last block
+          if (lane == 0) mbar_arrive(bar_sfe + 8 * slot);
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            sphase ^= 1;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
-        s = s_next;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
       if (!ok || !active) continue;
-      const int64_t at = m * p.ldc + nb * BN + half * 128;
-      const int n = min(128, ncols - half * 128);
+      if (split > 1) {   // this CTA's part of the sums, for the join below
+        float4* part = reinterpret_cast<float4*>(smem + row * kPartBytes) + col0 / 4;
+#pragma unroll
+        for (int i = 0; i < HN / 4; ++i)
+          part[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        continue;
+      }
+      const int64_t at = m * p.ldc + nb * BN + col0;
+      const int n = min(HN, ncols - col0);
       if (p.c_type == NVFP4MOE_BF16) store_row(static_cast<__nv_bfloat16*>(p.c) + at, acc, n, p.c_32B);
       else if (p.c_type == NVFP4MOE_F16) store_row(static_cast<__half*>(p.c) + at, acc, n, p.c_32B);
       else store_row(static_cast<float*>(p.c) + at, acc, n, p.c_32B);
     }
   }
 
+  if (split > 1) {
+    // The cluster's CTAs have each summed their blocks of K of one tile; eight
+    // columns of a row are joined by one thread, in the order of the blocks.
+    // Every CTA's part stays in shared memory until all have read it.
+    __syncwarp();
+    cluster_sync_all();
+    int e, nb, row0, rows, ncols;
+    sch.decode(first, e, nb, row0, rows, ncols);
+    join_parts<BN>(p, sbase, kPartBytes, rank, split, row0, rows, nb * BN, ncols, kThreads);
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -371,26 +560,427 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Tiles of at most NT activation rows (16, 32 or 64) x 128 weight rows, with
+// the operands exchanged: the weight rows are the MMA's M, the activation rows
+// its N, so that a lane holds one weight row and a block's products are NT
+// columns instead of 256. Reading them back costs NT / 256 of the time, four
+// buffers hide the hand-offs, and a tile of half the weight rows gives twice
+// the CTAs: with few rows the product is a stream of the weights from HBM, and
+// what counts is that every SM keeps loads in flight. One unit of work is one
+// tile and one range of its blocks of K (a cluster of `split` CTAs shares a
+// tile); a stage is small enough for two CTAs on an SM, so that one unit's
+// loads run under another's beginning and end. The sums leave through shared
+// memory, since a lane holds a column of C, joined over the cluster.
+// Warp roles (256 threads): 0 producer, 1 MMA, 2 factors, 4-7 epilogue. (Eight
+// epilogue warps for 64 rows measured the same: 14.5 us against 14.3 at
+// 64 x 4096 x 7168.)
+template <int NT>
+struct Few {
+  static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4;
+  static constexpr int BUFS = 4;             // at most STAGES (see bar_done)
+  static constexpr int W_BYTES = 128 * BK;   // 16 KB
+  static constexpr int T_BYTES = NT * BK;
+  static constexpr int OFF_T = STAGES * W_BYTES;
+  static constexpr int OFF_BAR = OFF_T + STAGES * T_BYTES;
+  static constexpr int SCALE_FLOATS = kScaleBlocks * NT;   // [block][row]
+  static constexpr int OFF_SCALE = OFF_BAR + 256;
+  static constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * SCALE_FLOATS * 4;
+  static constexpr int OFF_SCHED = OFF_MISC + 64;
+  static constexpr int PART_BYTES = 128 * 4 + 16;          // a row of partial sums
+  static constexpr uint32_t TMEM = BUFS * NT;
+  static_assert(NT * PART_BYTES <= OFF_BAR, "the partial sums lie in the ring");
+  static_assert(BUFS <= STAGES, "a barrier of a stage would complete twice unseen");
+};
+
+constexpr int kFewThreads = 256;
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                        const Params p) {
+  using C = Few<NT>;
+  constexpr int STAGES = C::STAGES, BUFS = C::BUFS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bar_full = sbase + C::OFF_BAR;         // STAGES: a stage's tiles landed
+  const uint32_t bar_done = bar_full + STAGES * 8;      // STAGES: its MMAs are done (as in fp8_gemm_kernel)
+  const uint32_t bar_acce = bar_done + STAGES * 8;      // BUFS: the epilogue has read a buffer
+  const uint32_t bar_sff = bar_acce + BUFS * 8;         // kScaleSlots: a group of factors is in shared memory
+  const uint32_t bar_sfe = bar_sff + kScaleSlots * 8;   // kScaleSlots: the epilogue has used it
+  const uint32_t bar_aux = bar_sfe + kScaleSlots * 8;   // MMA drain on abort
+  const uint32_t bar_never = bar_aux + 8;               // never arrived on (failure-path test)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
+  int32_t* start = reinterpret_cast<int32_t*>(smem + C::OFF_SCHED);
+  int32_t* tile_start = start + 2 * p.E;
+  const Sched sch{start, tile_start, p.E, p.NB, p.N, NT, 128};
+
+  if (tid == 0) {
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_w);
+  }
+  load_groups(p, start);
+  if (tid == 32) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_done + 8 * s, 1);
+    }
+    for (int b = 0; b < BUFS; ++b) mbar_init(bar_acce + 8 * b, 4);
+    for (int b = 0; b < kScaleSlots; ++b) {
+      mbar_init(bar_sff + 8 * b, 32);
+      mbar_init(bar_sfe + 8 * b, 4);
+    }
+    mbar_init(bar_aux, 1);
+    mbar_init(bar_never, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(smem_addr(tmem_slot), C::TMEM);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 0) scan_tiles(sch, tile_start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int split = p.split;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int unit = (int)blockIdx.x / split;
+  const bool any = unit < tile_start[p.E];   // the same for every CTA of a cluster
+  int e = 0, nb = 0, row0 = 0, rows = 0, ncols = 0;
+  if (any) sch.decode(unit, e, nb, row0, rows, ncols);
+  const int kb0 = p.KB * rank / split, kb1 = any ? p.KB * (rank + 1) / split : kb0;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t pol_w = p.w_once ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t pol_a = l2_policy_evict_last();
+    uint32_t stage = 0, phase = 0, filled = 0, fill_phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wait_bounded(bar_done + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 41)) {
+        ok = false;
+        break;
+      }
+      const uint32_t full = bar_full + 8 * stage;
+      mbar_arrive_expect_tx(full, C::W_BYTES + C::T_BYTES);
+      tma_load_2d(sbase + stage * C::W_BYTES, &tm_w, full, kb * BK, e * p.N + nb * 128, pol_w);
+      tma_load_2d(sbase + C::OFF_T + stage * C::T_BYTES, &tm_a, full, kb * BK, row0, pol_a);
+      filled |= 1u << stage;
+      fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok)   // copies still in flight complete before the CTA may exit
+      for (int s = 0; s < STAGES; ++s)
+        if ((filled >> s) & 1u) drain_wait(bar_full + 8 * s, (fill_phase >> s) & 1u);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const bool leader = elect_one();
+    uint32_t stage = 0, phase = 0, buf = 0, bphase = 1;
+    bool ok = true, issued = false;
+    const uint64_t wdesc0 = sdesc_kmajor_sw128(sbase);
+    const uint64_t tdesc0 = sdesc_kmajor_sw128(sbase + C::OFF_T);
+    if (p.test_stall && any)
+      ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 42));
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      ok = wait_bounded(bar_acce + 8 * buf, bphase, abort_flag, p.wait_limit_ns, p.status, 43) &&
+           wait_bounded(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 44);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t wd = wdesc0 + ((stage * C::W_BYTES) >> 4);
+      const uint64_t td = tdesc0 + ((stage * C::T_BYTES) >> 4);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk)
+          tc_mma_f8(tmem + buf * NT, wd + 2 * kk, td + 2 * kk, idesc_e4m3(128, NT), kk != 0 ? 1u : 0u);
+        tc_commit(bar_done + 8 * stage);
+      }
+      issued = true;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (++buf == BUFS) {
+        buf = 0;
+        bphase ^= 1;
+      }
+    }
+    if (!ok && issued && leader) {
+      tc_commit(bar_aux);
+      drain_wait(bar_aux, 0);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- factors
+    constexpr int R = (NT + 31) / 32;      // activation rows of a lane
+    uint32_t slot = 0, phase = 0;
+    const float* sa = p.a_sf + (int64_t)row0 * p.KB;
+    const float* sw = p.w_sf + ((int64_t)e * p.NB + nb) * p.KB;
+    for (int kg = kb0; kg < kb1; kg += kScaleBlocks) {
+      float a[R][kScaleBlocks];
+#pragma unroll
+      for (int k = 0; k < kScaleBlocks; ++k) {
+        const bool in = kg + k < kb1;
+        const float w = in ? __ldg(sw + kg + k) : 0.0f;
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          const int r = lane + 32 * h;
+          a[h][k] = in && r < rows ? __ldg(sa + (int64_t)r * p.KB + kg + k) * w : 0.0f;
+        }
+      }
+      if (!wait_bounded(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 46)) break;
+#pragma unroll
+      for (int k = 0; k < kScaleBlocks; ++k)
+#pragma unroll
+        for (int h = 0; h < R; ++h)
+          if (lane + 32 * h < NT) scales[slot * C::SCALE_FLOATS + k * NT + lane + 32 * h] = a[h][k];
+      mbar_arrive(bar_sff + 8 * slot);
+      if (++slot == kScaleSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    const int quad = warp & 3;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t stage = 0, phase = 0, buf = 0, slot = 0, sphase = 0;
+    bool ok = true;
+    float acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int in_group = (kb - kb0) % kScaleBlocks;
+      if (in_group == 0)
+        ok = wait_bounded(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 47);
+      ok = ok && wait_bounded(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 45);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* f = reinterpret_cast<const float4*>(scales + slot * C::SCALE_FLOATS + in_group * NT);
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        if (16 * c < rows) {
+          uint32_t v[16];
+          tc_ld16_wait(taddr + buf * NT + 16 * c, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 s = f[4 * c + q];
+            acc[16 * c + 4 * q] = fmaf(__uint_as_float(v[4 * q]), s.x, acc[16 * c + 4 * q]);
+            acc[16 * c + 4 * q + 1] = fmaf(__uint_as_float(v[4 * q + 1]), s.y, acc[16 * c + 4 * q + 1]);
+            acc[16 * c + 4 * q + 2] = fmaf(__uint_as_float(v[4 * q + 2]), s.z, acc[16 * c + 4 * q + 2]);
+            acc[16 * c + 4 * q + 3] = fmaf(__uint_as_float(v[4 * q + 3]), s.w, acc[16 * c + 4 * q + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
+      if (in_group == kScaleBlocks - 1 || kb + 1 == kb1) {
+        if (lane == 0) mbar_arrive(bar_sfe + 8 * slot);
+        if (++slot == kScaleSlots) {
+          slot = 0;
+          sphase ^= 1;
+        }
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (++buf == BUFS) buf = 0;
+    }
+    // every MMA of this CTA is done and its operands are read: the ring is free
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (i < rows)
+          *reinterpret_cast<float*>(smem + i * C::PART_BYTES + (quad * 32 + lane) * 4) = acc[i];
+    }
+  }
+
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+  join_parts<128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+// Clusters of `split` CTAs of a kernel that fit the device at once, asked once
+// per device (index: one per kernel).
+template <typename Kernel>
+int resident_clusters(Kernel kernel, int index, int threads, size_t smem, int split) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices][4][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::atomic<int>& slot = known[dev][index][split == 2 ? 0 : split == 4 ? 1 : 2];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)split, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = -1;
+    }
+    slot.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <typename Kernel, typename... Args>
+int launch_clusters(Kernel kernel, int64_t grid, int threads, size_t smem, int split, void* stream,
+                    const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = as_stream(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_status();
+}
+
+// How a kernel would run a product, and the time estimated for it.
+struct Plan {
+  int split = 1;   // CTAs (a cluster) to a tile
+  float us = 0;
+};
+
+// Where there are few tiles, each goes to a cluster of 2, 4 or 8 CTAs that
+// share its blocks of K, if all clusters run at once. A CTA takes `block` us a
+// block of K, joining the parts takes 0.5 us and 25 ns a row of the tile.
+// Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 1 x 4096 x 7168 32.4 /
+// 19.5 / 12.5 / 17.1 us (16 clusters of 8 were asked for and 15 fit), 128 x
+// 2048 x 7168 33.5 / 23.6 / 19.7 / 21.4, 128 x 512 x 512 7.6 / 10.8 / 10.7 /
+// 10.8.
+template <typename Resident>
+Plan plan(int64_t units, int KB, int rows, float block, float fixed, int sms, Resident resident) {
+  Plan best;
+  for (int split = 1; split <= kMaxSplit && split <= KB; split *= 2) {
+    if (split > 1 && units > resident(split)) break;
+    const float waves = units * split > sms ? (float)units * split / sms : 1.0f;
+    const float us = block * ((KB + split - 1) / split) * waves + (split > 1 ? 0.5f + 0.025f * rows : 0.0f) + fixed;
+    if (split == 1 || us < best.us) best = Plan{split, us};
+  }
+  return best;
+}
+
+// Activation tiles of tm rows, at most.
+int64_t tiles_of(const Params& p, int tm) {
+  if (!p.offsets) return ceil_div(p.M, tm);
+  return p.M / tm + (p.E < p.M ? p.E : p.M);
+}
+
+template <typename Kernel>
+bool allow_shared(Kernel kernel, size_t smem) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+template <int NT>
+struct FewLaunch {
+  size_t smem;
+  int64_t units;
+  Plan plan;
+  bool ok;
+  FewLaunch(const Params& p, int sms) {
+    smem = (size_t)Few<NT>::OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
+    units = tiles_of(p, NT) * p.NB;
+    ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, smem);
+    if (!ok) return;
+    // 0.22, 0.26 and 0.5 us a block (split 1, 56 blocks: 16.4, 18.8 and 29.1 us)
+    plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, 4.0f, sms,
+                          [&](int split) {
+                            return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3,
+                                                     kFewThreads, smem, split);
+                          });
+  }
+  int run(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t ldw, Params& p, void* stream) const {
+    CUtensorMap ma, mw;
+    if (!make_codes_map(&ma, a_codes, p.M, p.K, lda, NT) ||
+        !make_codes_map(&mw, w_codes, (int64_t)p.E * p.N, p.K, ldw, 128))
+      return NVFP4MOE_ERR_INVALID;
+    p.w_once = !p.offsets && p.M <= NT;
+    p.split = plan.split;
+    return launch_clusters(fp8_gemm_few_kernel<NT>, units * p.split, kFewThreads, smem, p.split, stream, ma, mw, p);
+  }
+};
+
 int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t ldw, Params& p, void* stream) {
+  p.status = device_status_word();
+  NVFP4_CHECK(p.status, NVFP4MOE_ERR_LAUNCH);
+  p.wait_limit_ns = wait_limit_ns();
+  p.test_stall = test_stall_on();
+  const int sms = device_num_sms();
+  NVFP4_CHECK(sms > 0, NVFP4MOE_ERR_LAUNCH);
+  const size_t smem = (size_t)OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
+  if (!allow_shared(fp8_gemm_kernel, smem)) return NVFP4MOE_ERR_LAUNCH;
+  const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
+  // (groups: the number of tiles is only known on the device; this kernel's
+  // CTAs then take them in turn)
+  Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, 0.5f, 6.0f, sms, [&](int split) {
+    return p.offsets ? 0 : resident_clusters(fp8_gemm_kernel, 0, kThreads, smem, split);
+  });
+  // Few rows: the other kernel where it is estimated to be faster (64 x 4096 x
+  // 7168 13.2 us against 16.9, 64 x 16384 x 7168 32.7 against 24.2). Rows of a
+  // group: the mean of the groups that can have one, and room for twice that.
+  const int rows = p.offsets ? 2 * (int)ceil_div(p.M, p.E < p.M ? p.E : p.M) : p.M;
+  if (rows <= 16) {
+    const FewLaunch<16> f(p, sms);
+    if (f.ok && f.plan.us <= tiles.us) return f.run(a_codes, lda, w_codes, ldw, p, stream);
+  } else if (rows <= 32) {
+    const FewLaunch<32> f(p, sms);
+    if (f.ok && f.plan.us <= tiles.us) return f.run(a_codes, lda, w_codes, ldw, p, stream);
+  } else if (rows <= 64) {
+    const FewLaunch<64> f(p, sms);
+    if (f.ok && f.plan.us <= tiles.us) return f.run(a_codes, lda, w_codes, ldw, p, stream);
+  }
   CUtensorMap ma[4], mb[2];
   const int boxes[4] = {16, 32, 64, 128};
   for (int i = 0; i < 4; ++i)
     if (!make_codes_map(&ma[i], a_codes, p.M, p.K, lda, boxes[i])) return NVFP4MOE_ERR_INVALID;
   for (int i = 0; i < 2; ++i)
     if (!make_codes_map(&mb[i], w_codes, (int64_t)p.E * p.N, p.K, ldw, 128 << i)) return NVFP4MOE_ERR_INVALID;
-  p.status = device_status_word();
-  NVFP4_CHECK(p.status, NVFP4MOE_ERR_LAUNCH);
-  p.wait_limit_ns = wait_limit_ns();
-  p.test_stall = test_stall_on();
-  const size_t smem = (size_t)OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
-  if (cudaFuncSetAttribute(fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return launch_status();
-  const int64_t most = (ceil_div(p.M, BM) + (p.E < p.M ? p.E : p.M)) * ceil_div(p.N, BN);   // upper bound of the tiles
-  const int sms = device_num_sms();
-  NVFP4_CHECK(sms > 0, NVFP4MOE_ERR_LAUNCH);
-  const unsigned grid = (unsigned)(most < sms ? most : sms);
-  fp8_gemm_kernel<<<grid, kThreads, smem, as_stream(stream)>>>(ma[0], ma[1], ma[2], ma[3], mb[0], mb[1], p);
-  return launch_status();
+  p.split = tiles.split;
+  const int64_t grid = p.split > 1 ? units * p.split : units < sms ? units : sms;
+  return launch_clusters(fp8_gemm_kernel, grid, kThreads, smem, p.split, stream, ma[0], ma[1], ma[2], ma[3], mb[0],
+                         mb[1], p);
 }
 
 int gemm(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, const uint8_t* w_codes, const float* w_sf,

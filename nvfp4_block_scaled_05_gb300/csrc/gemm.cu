@@ -58,6 +58,8 @@
 // in flight, frees its tensor memory and returns.
 #include "common.cuh"
 
+#include <atomic>
+
 namespace nvfp4moe {
 
 __device__ int g_status[2];  // [0]: NVFP4MOE_OK or NVFP4MOE_ERR_DEVICE_TIMEOUT, [1]: wait site
@@ -855,8 +857,17 @@ bool make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_
 }
 
 int* device_status_word() {
-  int* status = nullptr;
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(&status), g_status) == cudaSuccess ? status : nullptr;
+  // looked up once per device
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int*> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  int* status = known[dev].load(std::memory_order_relaxed);
+  if (!status) {
+    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&status), g_status) != cudaSuccess) return nullptr;
+    known[dev].store(status, std::memory_order_relaxed);
+  }
+  return status;
 }
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns; }

@@ -16,7 +16,6 @@
 namespace nvfp4moe {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxK = 16;
 
 struct Args {
@@ -72,9 +71,9 @@ __device__ __forceinline__ void load_slots(const Args& a, int64_t t, int64_t* ro
 }
 
 // Sums of KM values over the block in a fixed order; thread j < k writes slot j.
-template <int KM>
+template <int NT, int KM>
 __device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float (&dot)[KM], const int64_t* row) {
-  __shared__ float part[kThreads / 32][KM];
+  __shared__ float part[NT / 32][KM];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int j = 0; j < KM; ++j) {
@@ -87,14 +86,14 @@ __device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float
   if ((int)threadIdx.x < a.k) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i][threadIdx.x];
+    for (int i = 0; i < NT / 32; ++i) s += part[i][threadIdx.x];
     a.d_w[t * a.k + threadIdx.x] = row[threadIdx.x] >= 0 ? s : 0.0f;
   }
 }
 
 // One token's row to its k rows. KM >= k slots are unrolled.
-template <typename T, int V, int KM, bool kDot>
-__global__ void __launch_bounds__(kThreads) spread_kernel(const Args a) {
+template <typename T, int V, int KM, int NT, bool kDot>
+__global__ void __launch_bounds__(NT) spread_kernel(const Args a) {
   __shared__ int64_t row[kMaxK];
   __shared__ float wt[kMaxK];
   const int64_t t = blockIdx.x;
@@ -104,7 +103,9 @@ __global__ void __launch_bounds__(kThreads) spread_kernel(const Args a) {
 #pragma unroll
   for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
   const int64_t whole = a.K / V * V;
-  for (int64_t c = threadIdx.x * V; c < whole; c += kThreads * V) {
+  // the block's share of the columns (all of them with dots)
+  const int part = kDot ? 0 : blockIdx.y, parts = kDot ? 1 : gridDim.y;
+  for (int64_t c = (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
     using P = Pack<T, V>;
     const P x = *reinterpret_cast<const P*>(src + c);
     P o[KM];
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) spread_kernel(const Args a) {
       }
     }
   }
-  for (int64_t c = whole + threadIdx.x; c < a.K; c += kThreads) {   // the columns after the last whole pack
+  for (int64_t c = whole + part * NT + threadIdx.x; c < a.K; c += parts * NT) {   // after the last whole pack
     const float v = Elem<T>::get(src[c]);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
@@ -139,12 +140,12 @@ __global__ void __launch_bounds__(kThreads) spread_kernel(const Args a) {
       }
     }
   }
-  if constexpr (kDot) store_dots<KM>(a, t, dot, row);
+  if constexpr (kDot) store_dots<NT, KM>(a, t, dot, row);
 }
 
 // The weighted sum of a token's k rows, in j order, rounded once.
-template <typename T, int V, int KM, bool kDot>
-__global__ void __launch_bounds__(kThreads) collect_kernel(const Args a) {
+template <typename T, int V, int KM, int NT, bool kDot>
+__global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
   __shared__ int64_t row[kMaxK];
   __shared__ float wt[kMaxK];
   const int64_t t = blockIdx.x;
@@ -156,7 +157,9 @@ __global__ void __launch_bounds__(kThreads) collect_kernel(const Args a) {
 #pragma unroll
   for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
   const int64_t whole = a.K / V * V;
-  for (int64_t c = threadIdx.x * V; c < whole; c += kThreads * V) {
+  // the block's share of the columns (all of them with dots)
+  const int part = kDot ? 0 : blockIdx.y, parts = kDot ? 1 : gridDim.y;
+  for (int64_t c = (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
     using P = Pack<T, V>;
     P r[KM], x;
 #pragma unroll
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) collect_kernel(const Args a) {
     for (int i = 0; i < V; ++i) y.e[i] = Elem<T>::put(acc[i]);
     *reinterpret_cast<P*>(out + c) = y;
   }
-  for (int64_t c = whole + threadIdx.x; c < a.K; c += kThreads) {
+  for (int64_t c = whole + part * NT + threadIdx.x; c < a.K; c += parts * NT) {
     float acc = 0.0f;
     const float x = kDot ? Elem<T>::get(tok[c]) : 0.0f;
 #pragma unroll
@@ -195,19 +198,41 @@ __global__ void __launch_bounds__(kThreads) collect_kernel(const Args a) {
     }
     out[c] = Elem<T>::put(acc);
   }
-  if constexpr (kDot) store_dots<KM>(a, t, dot, row);
+  if constexpr (kDot) store_dots<NT, KM>(a, t, dot, row);
 }
 
+template <typename T, int V, int KM, int NT>
+void launch_nt(const Args& a, bool spread, bool dot, int parts, cudaStream_t s) {
+  const dim3 grid((unsigned)a.T, (unsigned)parts);
+  if (spread) {
+    if (dot) spread_kernel<T, V, KM, NT, true><<<grid, NT, 0, s>>>(a);
+    else spread_kernel<T, V, KM, NT, false><<<grid, NT, 0, s>>>(a);
+  } else {
+    if (dot) collect_kernel<T, V, KM, NT, true><<<grid, NT, 0, s>>>(a);
+    else collect_kernel<T, V, KM, NT, false><<<grid, NT, 0, s>>>(a);
+  }
+}
+
+// Blocks of 64 threads for the sums and the dot products: more blocks in
+// different phases to an SM (loads, stores, reduction), 8192 x 7168 BF16, k = 8:
+// sum 163 us against 187 with 256 threads, spread with dots 322 against 477,
+// sum with dots 184 against 215. The plain spread is better with 256 (162
+// against 176). With few tokens the columns of a token are divided over blocks,
+// or, where a block has to see all of them for its dot products, its 256
+// threads see them in fewer rounds (128 tokens: 6.1 against 11.9; from four
+// tokens an SM on, 608: 38.6 against 31.9).
 template <typename T, int V, int KM>
 void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
-  const unsigned grid = (unsigned)a.T;
-  if (spread) {
-    if (dot) spread_kernel<T, V, KM, true><<<grid, kThreads, 0, s>>>(a);
-    else spread_kernel<T, V, KM, false><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (dot) collect_kernel<T, V, KM, true><<<grid, kThreads, 0, s>>>(a);
-    else collect_kernel<T, V, KM, false><<<grid, kThreads, 0, s>>>(a);
-  }
+  const int64_t sms = device_num_sms();
+  const int64_t packs = ceil_div(a.K, V);
+  auto parts = [&](int threads, int64_t blocks) {
+    const int64_t most = ceil_div(packs, threads), want = ceil_div(blocks, a.T);
+    return (int)(most < want ? (most > 0 ? most : 1) : want);
+  };
+  if (dot ? a.T < 4 * sms : spread)
+    launch_nt<T, V, KM, 256>(a, spread, dot, dot ? 1 : parts(256, 4 * sms), s);
+  else
+    launch_nt<T, V, KM, 64>(a, spread, dot, dot ? 1 : parts(64, 16 * sms), s);
 }
 
 // 16-byte accesses where every row of every operand starts on a 16-byte
