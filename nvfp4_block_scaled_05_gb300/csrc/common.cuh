@@ -545,7 +545,7 @@ template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                              uint64_t limit_ns, int* status, int site, uint32_t peer_abort = 0) {
   auto probe = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (probe()) return true;
+  if (__builtin_expect(probe(), 1)) return true;
   // the clock is read only now and then: a read of it on every wait that does
   // not succeed at once would sit on the path of each hand-off between warps
   uint64_t t0 = 0;

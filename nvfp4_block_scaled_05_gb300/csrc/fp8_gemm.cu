@@ -46,11 +46,9 @@ constexpr int A_BYTES = BM * BK;         // 16 KB
 constexpr int B_BYTES = BN * BK;         // 32 KB
 constexpr int OFF_B = STAGES * A_BYTES;
 constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
-constexpr int kScaleBlocks = 4;          // blocks of K whose scales change hands together
-constexpr int kScaleSlots = 4;           // such groups on their way
-constexpr int SCALE_FLOATS = 2 * kScaleBlocks * BM;   // of one group: [half][block][row]
-constexpr int OFF_SCALE = OFF_BAR + 256;
-constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * SCALE_FLOATS * 4;
+constexpr int kScaleSlots = 8;           // blocks of K whose factors are in shared memory (see bar_done)
+constexpr int OFF_SCALE = OFF_BAR + 256; // [slot][half][row]
+constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * 2 * BM * 4;
 constexpr int OFF_SCHED = OFF_MISC + 64;
 constexpr uint32_t TMEM_COLS = 512;      // two buffers of 256 columns
 constexpr int kPartBytes = BN * 4 + 16;  // a row of partial sums in shared memory; 16 bytes against bank conflicts
@@ -241,7 +239,7 @@ __device__ __forceinline__ void store_row(T* out, const float (&acc)[HN], int n,
 // sums of `split` CTAs (rows of TN f32, part_bytes apart, at the same place in
 // the shared memory of each): eight columns of a row by one thread, added in
 // the order of the blocks of K.
-template <int TN>
+template <typename T, int TN>
 __device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int part_bytes, int rank, int split,
                                            int row0, int rows, int col0, int ncols, int threads) {
   for (int i = rank * threads + threadIdx.x; i < rows * (TN / 8); i += split * threads) {
@@ -265,14 +263,14 @@ __device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int 
       for (int r = 1; r < kMaxSplit; ++r)
         if (r < split) v[k] += w[r][k];
     }
-    const int64_t at = (int64_t)(row0 + row) * p.ldc + col0 + col;
-    const int n = min(8, ncols - col);
-    if (p.c_type == NVFP4MOE_BF16) store8(static_cast<__nv_bfloat16*>(p.c) + at, v, n, p.c_32B);
-    else if (p.c_type == NVFP4MOE_F16) store8(static_cast<__half*>(p.c) + at, v, n, p.c_32B);
-    else store8(static_cast<float*>(p.c) + at, v, n, p.c_32B);
+    store8(static_cast<T*>(p.c) + (int64_t)(row0 + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_32B);
   }
 }
 
+// T: the type of C (a kernel for each, since code for all three in one left the
+// epilogue's loop short of registers: 125.7 us against 109.1 at 4096 x 4096 x
+// 7168).
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a16, const __grid_constant__ CUtensorMap tm_a32,
                     const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a128,
@@ -284,16 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bar_full = sbase + OFF_BAR;            // STAGES: a stage's tiles landed
-  // STAGES: the stage's MMAs are done. The epilogue waits for it before it
-  // reads the products, the producer before it fills the stage again: one
-  // commit a block serves both. It cannot complete again before the epilogue
-  // has seen it: that takes the MMAs of STAGES blocks later, which wait for
-  // the epilogue's release of a buffer that it gives only after this block.
+  // STAGES: the stage's MMAs are done (one commit) and its factors are in
+  // shared memory (the two scale warps). The epilogue waits for it before it
+  // reads the products, the producer before it fills the stage again, a scale
+  // warp before it writes the factors of STAGES blocks later. It cannot
+  // complete again before the epilogue has seen it: that takes the MMAs of
+  // STAGES blocks later, which wait for the epilogue's release of a buffer
+  // that it gives only after this block. For the same reason the factors of
+  // all but the last six blocks are used up when a barrier completes, and
+  // eight slots need no barrier of their own.
   const uint32_t bar_done = bar_full + STAGES * 8;
   const uint32_t bar_acce = bar_done + STAGES * 8;      // 2: the epilogue has read buffer b, columns 256 b on
-  const uint32_t bar_sff = bar_acce + 16;               // kScaleSlots: a group of scales is in shared memory
-  const uint32_t bar_sfe = bar_sff + kScaleSlots * 8;   // kScaleSlots: the epilogue has read it
-  const uint32_t bar_aux = bar_sfe + kScaleSlots * 8;   // MMA drain on abort
+  const uint32_t bar_aux = bar_acce + 16;               // MMA drain on abort
   const uint32_t bar_never = bar_aux + 8;               // never arrived on (failure-path test)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -306,13 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_done + 8 * s, 1);
+      mbar_init(bar_done + 8 * s, 3);
     }
     for (int b = 0; b < 2; ++b) mbar_init(bar_acce + 8 * b, 8);
-    for (int b = 0; b < kScaleSlots; ++b) {
-      mbar_init(bar_sff + 8 * b, 64);
-      mbar_init(bar_sfe + 8 * b, 8);
-    }
     mbar_init(bar_aux, 1);
     mbar_init(bar_never, 1);
     *abort_flag = 0;
@@ -383,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop and one elected lane issues, so that the
     // descriptors stay in uniform registers.
     const bool leader = elect_one();
-    uint32_t stage = 0, phase = 0, g = 0;
+    uint32_t g = 0;
     bool ok = true, issued = false;
     const uint64_t adesc0 = sdesc_kmajor_sw128(sbase);
     const uint64_t bdesc0 = sdesc_kmajor_sw128(sbase + OFF_B);
@@ -394,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sch.decode(t, e, nb, row0, rows, ncols);
       const uint32_t idesc = idesc_e4m3(BM, (ncols + 15) / 16 * 16);
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const uint32_t buf = g & 1u;
-        ok = wait_bounded(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 34) &&
+        const uint32_t stage = g % STAGES, buf = g & 1u;
+        ok = wait_bounded(bar_full + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns, p.status, 34) &&
              wait_bounded(bar_acce + 8 * buf, ((g >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 33);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        if (__builtin_expect(!ok, 0)) break;
         tc_fence_after();
         const uint64_t ad = adesc0 + ((stage * A_BYTES) >> 4);
         const uint64_t bd = bdesc0 + ((stage * B_BYTES) >> 4);
@@ -409,10 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(bar_done + 8 * stage);
         }
         issued = true;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
     }
     if (!ok && issued && leader) {   // tensor-core work in flight completes before the tensor memory is freed
@@ -421,13 +413,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2 || warp == 3) {
     // ---------------------------------------------------------------- scales
-    // Thread i makes the factors of rows i and i + 64, for both column halves
-    // (a weight block each), four blocks of K at a time and up to four such
-    // groups ahead. The epilogue then reads one word a block: with the loads
-    // in the epilogue, every block waited for them (linear 4096 x 4096 x 7168:
-    // 147 us against 114 with a constant in their place).
+    // Thread i makes the factors of rows i and i + 64 for both column halves
+    // (a weight block each), up to four blocks ahead of the epilogue, which
+    // then reads one word a block; the scales of the next four blocks are on
+    // their way meanwhile. With the loads in the epilogue, every block waited
+    // for them (linear 4096 x 4096 x 7168: 147 us against 114 with a constant
+    // in their place).
     const int i = tid - 64;
-    uint32_t slot = 0, phase = 0;
+    uint32_t g = 0;
     bool ok = true;
     for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
@@ -435,33 +428,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* sa = p.a_sf + (int64_t)row0 * KB;
       const float* sw0 = p.w_sf + ((int64_t)e * p.NB + nb * 2) * KB;
       const float* sw1 = ncols > HN ? sw0 + KB : sw0;
-      for (int kg = kb0; kg < kb1; kg += kScaleBlocks) {
-        float a[2][kScaleBlocks], w0[kScaleBlocks], w1[kScaleBlocks];
+      float a0[4], a1[4], w0[4], w1[4];
+      auto fetch = [&](int kg) {
 #pragma unroll
-        for (int k = 0; k < kScaleBlocks; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const bool in = kg + k < kb1;
           w0[k] = in ? __ldg(sw0 + kg + k) : 0.0f;
           w1[k] = in ? __ldg(sw1 + kg + k) : 0.0f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            a[h][k] = in && i + 64 * h < rows ? __ldg(sa + (int64_t)(i + 64 * h) * KB + kg + k) : 0.0f;
+          a0[k] = in && i < rows ? __ldg(sa + (int64_t)i * KB + kg + k) : 0.0f;
+          a1[k] = in && i + 64 < rows ? __ldg(sa + (int64_t)(i + 64) * KB + kg + k) : 0.0f;
         }
-        if (!wait_bounded(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 36)) {
-          ok = false;
-          break;
+      };
+      fetch(kb0);
+      for (int kg = kb0; ok && kg < kb1; kg += 4) {
+        float f[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k][0] = a0[k] * w0[k];
+          f[k][1] = a1[k] * w0[k];
+          f[k][2] = a0[k] * w1[k];
+          f[k][3] = a1[k] * w1[k];
         }
-        float* out = scales + slot * SCALE_FLOATS + i;
+        fetch(kg + 4);
 #pragma unroll
-        for (int k = 0; k < kScaleBlocks; ++k)
+        for (int k = 0; k < 4; ++k) {
+          if (kg + k < kb1) {
+            const uint32_t bar = bar_done + 8 * (g % STAGES);
+            ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar, (g / STAGES & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 36));
+            if (!ok) break;
+            float* out = scales + (g % kScaleSlots) * (2 * BM) + i;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            out[k * BM + 64 * h] = a[h][k] * w0[k];
-            out[(kScaleBlocks + k) * BM + 64 * h] = a[h][k] * w1[k];
+            for (int h = 0; h < 4; ++h) out[64 * h] = f[k][h];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            ++g;
           }
-        mbar_arrive(bar_sff + 8 * slot);
-        if (++slot == kScaleSlots) {
-          slot = 0;
-          phase ^= 1;
         }
       }
     }
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int col0 = half * HN;             // its columns are those of one 128-wide weight block
     const int row = quad * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    uint32_t g = 0, stage = 0, phase = 0, slot = 0, sphase = 0;
+    uint32_t g = 0;
     bool ok = true;
     for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
@@ -484,15 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < HN; ++i) acc[i] = 0.0f;
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const uint32_t buf = g & 1u;
-        const int in_group = (kb - kb0) % kScaleBlocks;
-        if (in_group == 0)
-          ok = wait_bounded(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 37);
-        const float s = scales[slot * SCALE_FLOATS + (half * kScaleBlocks + in_group) * BM + row];
-        ok = ok && wait_bounded(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 35);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        const uint32_t stage = g % STAGES, buf = g & 1u;
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_done + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns,
+                                                  p.status, 35));
+        if (__builtin_expect(!ok, 0)) break;
         tc_fence_after();
+        const float s = scales[(g % kScaleSlots) * (2 * BM) + half * BM + row];
         if (live) {
 #pragma unroll
           for (int c = 0; c < HN / 16; ++c) {
@@ -510,18 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
         }
-        if (in_group == kScaleBlocks - 1 || kb + 1 == kb1) {
-          __syncwarp();   // every lane has used its scale of the group's last block
-          if (lane == 0) mbar_arrive(bar_sfe + 8 * slot);
-          if (++slot == kScaleSlots) {
-            slot = 0;
-            sphase ^= 1;
-          }
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
       if (!ok || !active) continue;
       if (split > 1) {   // this CTA's part of the sums, for the join below
@@ -531,11 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         continue;
       }
-      const int64_t at = m * p.ldc + nb * BN + col0;
-      const int n = min(HN, ncols - col0);
-      if (p.c_type == NVFP4MOE_BF16) store_row(static_cast<__nv_bfloat16*>(p.c) + at, acc, n, p.c_32B);
-      else if (p.c_type == NVFP4MOE_F16) store_row(static_cast<__half*>(p.c) + at, acc, n, p.c_32B);
-      else store_row(static_cast<float*>(p.c) + at, acc, n, p.c_32B);
+      store_row(static_cast<T*>(p.c) + m * p.ldc + nb * BN + col0, acc, min(HN, ncols - col0), p.c_32B);
     }
   }
 
@@ -547,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     int e, nb, row0, rows, ncols;
     sch.decode(first, e, nb, row0, rows, ncols);
-    join_parts<BN>(p, sbase, kPartBytes, rank, split, row0, rows, nb * BN, ncols, kThreads);
+    join_parts<T, BN>(p, sbase, kPartBytes, rank, split, row0, rows, nb * BN, ncols, kThreads);
     __syncwarp();
     cluster_sync_all();
   }
@@ -584,9 +566,11 @@ struct Few {
   static constexpr int T_BYTES = NT * BK;
   static constexpr int OFF_T = STAGES * W_BYTES;
   static constexpr int OFF_BAR = OFF_T + STAGES * T_BYTES;
-  static constexpr int SCALE_FLOATS = kScaleBlocks * NT;   // [block][row]
+  // factors change hands four blocks at a time, four such groups on their way
+  static constexpr int SBLOCKS = 4, SSLOTS = 4;
+  static constexpr int SCALE_FLOATS = SBLOCKS * NT;        // [block][row]
   static constexpr int OFF_SCALE = OFF_BAR + 256;
-  static constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * SCALE_FLOATS * 4;
+  static constexpr int OFF_MISC = OFF_SCALE + SSLOTS * SCALE_FLOATS * 4;
   static constexpr int OFF_SCHED = OFF_MISC + 64;
   static constexpr int PART_BYTES = 128 * 4 + 16;          // a row of partial sums
   static constexpr uint32_t TMEM = BUFS * NT;
@@ -610,9 +594,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t bar_full = sbase + C::OFF_BAR;         // STAGES: a stage's tiles landed
   const uint32_t bar_done = bar_full + STAGES * 8;      // STAGES: its MMAs are done (as in fp8_gemm_kernel)
   const uint32_t bar_acce = bar_done + STAGES * 8;      // BUFS: the epilogue has read a buffer
-  const uint32_t bar_sff = bar_acce + BUFS * 8;         // kScaleSlots: a group of factors is in shared memory
-  const uint32_t bar_sfe = bar_sff + kScaleSlots * 8;   // kScaleSlots: the epilogue has used it
-  const uint32_t bar_aux = bar_sfe + kScaleSlots * 8;   // MMA drain on abort
+  const uint32_t bar_sff = bar_acce + BUFS * 8;         // SSLOTS: a group of factors is in shared memory
+  const uint32_t bar_sfe = bar_sff + C::SSLOTS * 8;   // SSLOTS: the epilogue has used it
+  const uint32_t bar_aux = bar_sfe + C::SSLOTS * 8;   // MMA drain on abort
   const uint32_t bar_never = bar_aux + 8;               // never arrived on (failure-path test)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -632,7 +616,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       mbar_init(bar_done + 8 * s, 1);
     }
     for (int b = 0; b < BUFS; ++b) mbar_init(bar_acce + 8 * b, 4);
-    for (int b = 0; b < kScaleSlots; ++b) {
+    for (int b = 0; b < C::SSLOTS; ++b) {
       mbar_init(bar_sff + 8 * b, 32);
       mbar_init(bar_sfe + 8 * b, 4);
     }
@@ -728,10 +712,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     uint32_t slot = 0, phase = 0;
     const float* sa = p.a_sf + (int64_t)row0 * p.KB;
     const float* sw = p.w_sf + ((int64_t)e * p.NB + nb) * p.KB;
-    for (int kg = kb0; kg < kb1; kg += kScaleBlocks) {
-      float a[R][kScaleBlocks];
+    for (int kg = kb0; kg < kb1; kg += C::SBLOCKS) {
+      float a[R][C::SBLOCKS];
 #pragma unroll
-      for (int k = 0; k < kScaleBlocks; ++k) {
+      for (int k = 0; k < C::SBLOCKS; ++k) {
         const bool in = kg + k < kb1;
         const float w = in ? __ldg(sw + kg + k) : 0.0f;
 #pragma unroll
@@ -742,12 +726,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
       if (!wait_bounded(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 46)) break;
 #pragma unroll
-      for (int k = 0; k < kScaleBlocks; ++k)
+      for (int k = 0; k < C::SBLOCKS; ++k)
 #pragma unroll
         for (int h = 0; h < R; ++h)
           if (lane + 32 * h < NT) scales[slot * C::SCALE_FLOATS + k * NT + lane + 32 * h] = a[h][k];
       mbar_arrive(bar_sff + 8 * slot);
-      if (++slot == kScaleSlots) {
+      if (++slot == C::SSLOTS) {
         slot = 0;
         phase ^= 1;
       }
@@ -762,7 +746,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
     for (int kb = kb0; kb < kb1; ++kb) {
-      const int in_group = (kb - kb0) % kScaleBlocks;
+      const int in_group = (kb - kb0) % C::SBLOCKS;
       if (in_group == 0)
         ok = wait_bounded(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 47);
       ok = ok && wait_bounded(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 45);
@@ -788,9 +772,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
-      if (in_group == kScaleBlocks - 1 || kb + 1 == kb1) {
+      if (in_group == C::SBLOCKS - 1 || kb + 1 == kb1) {
         if (lane == 0) mbar_arrive(bar_sfe + 8 * slot);
-        if (++slot == kScaleSlots) {
+        if (++slot == C::SSLOTS) {
           slot = 0;
           sphase ^= 1;
         }
@@ -813,7 +797,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncwarp();
   if (split > 1) cluster_sync_all();
   else __syncthreads();
-  join_parts<128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+  if (p.c_type == NVFP4MOE_BF16)
+    join_parts<__nv_bfloat16, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+  else if (p.c_type == NVFP4MOE_F16)
+    join_parts<__half, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+  else
+    join_parts<float, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
   __syncwarp();
   if (split > 1) cluster_sync_all();
   tc_fence_before();
@@ -949,13 +938,16 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   p.test_stall = test_stall_on();
   const int sms = device_num_sms();
   NVFP4_CHECK(sms > 0, NVFP4MOE_ERR_LAUNCH);
+  auto kernel = p.c_type == NVFP4MOE_BF16  ? fp8_gemm_kernel<__nv_bfloat16>
+                : p.c_type == NVFP4MOE_F16 ? fp8_gemm_kernel<__half>
+                                           : fp8_gemm_kernel<float>;
   const size_t smem = (size_t)OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
-  if (!allow_shared(fp8_gemm_kernel, smem)) return NVFP4MOE_ERR_LAUNCH;
+  if (!allow_shared(kernel, smem)) return NVFP4MOE_ERR_LAUNCH;
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
   Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, 0.5f, 6.0f, sms, [&](int split) {
-    return p.offsets ? 0 : resident_clusters(fp8_gemm_kernel, 0, kThreads, smem, split);
+    return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, smem, split);
   });
   // Few rows: the other kernel where it is estimated to be faster (64 x 4096 x
   // 7168 13.2 us against 16.9, 64 x 16384 x 7168 32.7 against 24.2). Rows of a
@@ -979,7 +971,7 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
     if (!make_codes_map(&mb[i], w_codes, (int64_t)p.E * p.N, p.K, ldw, 128 << i)) return NVFP4MOE_ERR_INVALID;
   p.split = tiles.split;
   const int64_t grid = p.split > 1 ? units * p.split : units < sms ? units : sms;
-  return launch_clusters(fp8_gemm_kernel, grid, kThreads, smem, p.split, stream, ma[0], ma[1], ma[2], ma[3], mb[0],
+  return launch_clusters(kernel, grid, kThreads, smem, p.split, stream, ma[0], ma[1], ma[2], ma[3], mb[0],
                          mb[1], p);
 }
 
