@@ -38,23 +38,27 @@ namespace {
 constexpr int BM = 128;
 constexpr int BN = 256;
 constexpr int BK = 128;                  // K elements (bytes) per stage: one scale block
-constexpr int STAGES = 4;
 constexpr int HN = BN / 2;               // columns of one epilogue warpgroup
 constexpr int kEpiWarp0 = 4;             // the first of two epilogue warpgroups
 constexpr int kThreads = 32 * (kEpiWarp0 + 8);
+constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK;         // 16 KB
 constexpr int B_BYTES = BN * BK;         // 32 KB
+constexpr int kScaleSlots = 8;           // blocks of K whose factors are in shared memory (see bar_done)
+constexpr int kOutRow = 32;              // bytes of a row of C that an epilogue warp stages at a time,
+constexpr int kOutPitch = kOutRow + 16;  // and their distance (16 bytes against bank conflicts)
 constexpr int OFF_B = STAGES * A_BYTES;
 constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
-constexpr int kScaleSlots = 8;           // blocks of K whose factors are in shared memory (see bar_done)
-constexpr int OFF_SCALE = OFF_BAR + 256; // [slot][half][row]
-constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * 2 * BM * 4;
+constexpr int OFF_SCALE = OFF_BAR + 256;                       // [slot][half][row]
+constexpr int OFF_OUT = OFF_SCALE + kScaleSlots * 2 * BM * 4;  // 32 staged rows of each epilogue warp
+constexpr int OFF_MISC = OFF_OUT + 8 * 32 * kOutPitch;
 constexpr int OFF_SCHED = OFF_MISC + 64;
 constexpr uint32_t TMEM_COLS = 512;      // two buffers of 256 columns
 constexpr int kPartBytes = BN * 4 + 16;  // a row of partial sums in shared memory; 16 bytes against bank conflicts
 constexpr int kMaxSplit = 8;
 constexpr int kMaxGroups = 1024;
 static_assert(BM * kPartBytes <= OFF_BAR, "the partial sums lie in the ring");
+static_assert(OFF_SCHED + 4 * (3 * kMaxGroups + 1) + 1024 <= 232448, "shared memory budget");
 
 struct Params {
   const float* a_sf;          // (M, KB)
@@ -68,6 +72,7 @@ struct Params {
   int w_once;                 // few rows: every weight row is read by one tile only
   int split;                  // CTAs (a cluster) that share a tile's blocks of K
   int c_32B;                  // c and ldc allow 32-byte stores
+  int c_unit;                 // bytes (2 to 16) that every row of c can be stored in units of
   uint64_t wait_limit_ns;
   int* status;
   int test_stall;             // test hook: the MMA issuer first waits on a barrier nobody arrives on
@@ -186,10 +191,10 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// The first n of 16 values to out: 32-byte stores where the row allows them.
+// The first n of 16 values to out, which is 32-byte aligned.
 template <typename T>
-__device__ __forceinline__ void store16(T* out, const float* v, int n, bool wide) {
-  if (wide && n >= 16) {
+__device__ __forceinline__ void store16(T* out, const float* v, int n) {
+  if (n >= 16) {
     if constexpr (sizeof(T) == 2) {
       uint32_t w[8];
 #pragma unroll
@@ -210,29 +215,77 @@ __device__ __forceinline__ void store16(T* out, const float* v, int n, bool wide
   }
 }
 
-// The first n of 8 values to out: 16-byte stores where the rows allow them.
 template <typename T>
-__device__ __forceinline__ void store8(T* out, const float (&v)[8], int n, bool wide) {
-  if (wide && n >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(out) = make_uint4(pack2(out, v[0], v[1]), pack2(out, v[2], v[3]),
-                                                  pack2(out, v[4], v[5]), pack2(out, v[6], v[7]));
-    } else {
-      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
+__device__ __forceinline__ void store_row(T* out, const float (&acc)[HN], int n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) put(out + i, v[i]);
-  }
+  for (int j = 0; j < HN / 16; ++j)
+    if (16 * j < n) store16(out + 16 * j, acc + 16 * j, n - 16 * j);
+}
+
+// Eight values of a row of C from column `col` of `ncols` on, in the units that
+// the rows allow (ncols is whole units).
+template <typename U, typename T>
+__device__ __forceinline__ void store_units(T* out, const T (&v)[8], int n) {
+  constexpr int PER = sizeof(U) / sizeof(T) > 0 ? sizeof(U) / sizeof(T) : 1;
+#pragma unroll
+  for (int i = 0; i < 8; i += PER)
+    if (i < n) *reinterpret_cast<U*>(out + i) = *reinterpret_cast<const U*>(v + i);
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row(T* out, const float (&acc)[HN], int n, bool wide) {
+__device__ __forceinline__ void store8(T* out, const float (&f)[8], int n, int unit) {
+  alignas(16) T v[8];
 #pragma unroll
-  for (int j = 0; j < HN / 16; ++j)
-    if (16 * j < n) store16(out + 16 * j, acc + 16 * j, n - 16 * j, wide);
+  for (int i = 0; i < 8; ++i) put(v + i, f[i]);
+  if (unit == 16) store_units<uint4>(out, v, n);
+  else if (unit == 8) store_units<uint2>(out, v, n);
+  else if (unit == 4 || sizeof(T) == 4) store_units<uint32_t>(out, v, n);
+  else store_units<uint16_t>(out, v, n);
+}
+
+// One unit from shared to global memory.
+template <typename U>
+__device__ __forceinline__ void copy_out(uint8_t* c, int64_t ld_bytes, const uint8_t* staged, int rows, int bytes,
+                                         int lane) {
+  constexpr int PER_ROW = kOutRow / sizeof(U);
+#pragma unroll 4
+  for (int i = 0; i < PER_ROW; ++i) {
+    const int u = i * 32 + lane, r = u / PER_ROW, b = u % PER_ROW * (int)sizeof(U);
+    if (r < rows && b < bytes)
+      *reinterpret_cast<U*>(c + r * ld_bytes + b) = *reinterpret_cast<const U*>(staged + r * kOutPitch + b);
+  }
+}
+
+// A warp's 32 rows x HN columns of C, of which `rows` and `cols` exist, where
+// the rows of C are not whole 32-byte sectors; lane r holds row r. Its own
+// stores would be an element each, to 32 rows at a time (4096 x 4095 x 2048
+// took 183 us, 4096 x 4096 x 2048 41), so 32 bytes of each row at a time go
+// through shared memory and leave as pieces of rows.
+template <typename T>
+__device__ __forceinline__ void store_tile(T* c, int64_t ldc, const float (&acc)[HN], int rows, int cols, int unit,
+                                           uint8_t* staged, int lane) {
+  constexpr int N = kOutRow / (int)sizeof(T);   // columns at a time
+#pragma unroll
+  for (int p = 0; p < HN / N; ++p) {
+    if (p * N < cols) {   // the whole warp
+#pragma unroll
+      for (int q = 0; q < kOutRow / 16; ++q) {
+        alignas(16) T v[16 / sizeof(T)];
+#pragma unroll
+        for (int i = 0; i < 16 / (int)sizeof(T); ++i) put(v + i, acc[p * N + q * (16 / (int)sizeof(T)) + i]);
+        *reinterpret_cast<uint4*>(staged + lane * kOutPitch + 16 * q) = *reinterpret_cast<const uint4*>(v);
+      }
+      __syncwarp();
+      uint8_t* out = reinterpret_cast<uint8_t*>(c + p * N);
+      const int64_t ld = ldc * (int64_t)sizeof(T);
+      const int bytes = min(N, cols - p * N) * (int)sizeof(T);
+      if (unit == 16) copy_out<uint4>(out, ld, staged, rows, bytes, lane);
+      else if (unit == 8) copy_out<uint2>(out, ld, staged, rows, bytes, lane);
+      else if (unit == 4) copy_out<uint32_t>(out, ld, staged, rows, bytes, lane);
+      else copy_out<uint16_t>(out, ld, staged, rows, bytes, lane);
+      __syncwarp();
+    }
+  }
 }
 
 // C's rows [row0, row0 + rows), columns [col0, col0 + ncols) from the partial
@@ -263,14 +316,14 @@ __device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int 
       for (int r = 1; r < kMaxSplit; ++r)
         if (r < split) v[k] += w[r][k];
     }
-    store8(static_cast<T*>(p.c) + (int64_t)(row0 + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_32B);
+    store8(static_cast<T*>(p.c) + (int64_t)(row0 + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_unit);
   }
 }
 
-// T: the type of C (a kernel for each, since code for all three in one left the
-// epilogue's loop short of registers: 125.7 us against 109.1 at 4096 x 4096 x
-// 7168).
-template <typename T>
+// T: the type of C; kWhole: its rows are whole 32-byte sectors. A kernel for
+// each, since code for all in one leaves the epilogue's loop short of
+// registers: 125.7 us against 109.1 at 4096 x 4096 x 7168 with three types.
+template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a16, const __grid_constant__ CUtensorMap tm_a32,
                     const __grid_constant__ CUtensorMap tm_a64, const __grid_constant__ CUtensorMap tm_a128,
@@ -479,8 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e, nb, row0, rows, ncols;
       sch.decode(t, e, nb, row0, rows, ncols);
       const bool live = quad * 32 < rows && col0 < ncols;   // the whole warp
-      const bool active = row < rows && col0 < ncols;
-      const int64_t m = row0 + min(row, rows - 1);
       float acc[HN];
 #pragma unroll
       for (int i = 0; i < HN; ++i) acc[i] = 0.0f;
@@ -509,15 +560,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
         }
       }
-      if (!ok || !active) continue;
+      if (!ok || !live) continue;
       if (split > 1) {   // this CTA's part of the sums, for the join below
+        if (row >= rows) continue;
         float4* part = reinterpret_cast<float4*>(smem + row * kPartBytes) + col0 / 4;
 #pragma unroll
         for (int i = 0; i < HN / 4; ++i)
           part[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         continue;
       }
-      store_row(static_cast<T*>(p.c) + m * p.ldc + nb * BN + col0, acc, min(HN, ncols - col0), p.c_32B);
+      T* out = static_cast<T*>(p.c) + (int64_t)(row0 + quad * 32) * p.ldc + nb * BN + col0;
+      const int n = min(HN, ncols - col0);
+      if constexpr (kWhole) {
+        if (row < rows) store_row(out + lane * p.ldc, acc, n);
+      } else {
+        store_tile(out, p.ldc, acc, min(32, rows - quad * 32), n, p.c_unit,
+                   smem + OFF_OUT + (warp - kEpiWarp0) * 32 * kOutPitch, lane);
+      }
     }
   }
 
@@ -938,9 +997,10 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   p.test_stall = test_stall_on();
   const int sms = device_num_sms();
   NVFP4_CHECK(sms > 0, NVFP4MOE_ERR_LAUNCH);
-  auto kernel = p.c_type == NVFP4MOE_BF16  ? fp8_gemm_kernel<__nv_bfloat16>
-                : p.c_type == NVFP4MOE_F16 ? fp8_gemm_kernel<__half>
-                                           : fp8_gemm_kernel<float>;
+  auto kernel = p.c_type == NVFP4MOE_BF16
+                    ? (p.c_32B ? fp8_gemm_kernel<__nv_bfloat16, true> : fp8_gemm_kernel<__nv_bfloat16, false>)
+                : p.c_type == NVFP4MOE_F16 ? (p.c_32B ? fp8_gemm_kernel<__half, true> : fp8_gemm_kernel<__half, false>)
+                                           : (p.c_32B ? fp8_gemm_kernel<float, true> : fp8_gemm_kernel<float, false>);
   const size_t smem = (size_t)OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
   if (!allow_shared(kernel, smem)) return NVFP4MOE_ERR_LAUNCH;
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
@@ -1003,6 +1063,8 @@ int gemm(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, cons
   p.c_type = c_type;
   p.ldc = ldc;
   p.c_32B = aligned(c, 32) && ldc * es % 32 == 0;
+  p.c_unit = 16;
+  while (p.c_unit > es && !(aligned(c, p.c_unit) && ldc * es % p.c_unit == 0 && N * es % p.c_unit == 0)) p.c_unit /= 2;
   return launch(a_codes, lda, w_codes, ldw, p, stream);
 }
 
