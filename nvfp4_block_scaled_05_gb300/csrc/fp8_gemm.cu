@@ -248,7 +248,7 @@ template <typename U>
 __device__ __forceinline__ void copy_out(uint8_t* c, int64_t ld_bytes, const uint8_t* staged, int rows, int bytes,
                                          int lane) {
   constexpr int PER_ROW = kOutRow / sizeof(U);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < PER_ROW; ++i) {
     const int u = i * 32 + lane, r = u / PER_ROW, b = u % PER_ROW * (int)sizeof(U);
     if (r < rows && b < bytes)
@@ -930,19 +930,26 @@ struct Plan {
 };
 
 // Where there are few tiles, each goes to a cluster of 2, 4 or 8 CTAs that
-// share its blocks of K, if all clusters run at once. A CTA takes `block` us a
-// block of K, joining the parts takes 0.5 us and 25 ns a row of the tile.
-// Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 1 x 4096 x 7168 32.4 /
-// 19.5 / 12.5 / 17.1 us (16 clusters of 8 were asked for and 15 fit), 128 x
-// 2048 x 7168 33.5 / 23.6 / 19.7 / 21.4, 128 x 512 x 512 7.6 / 10.8 / 10.7 /
-// 10.8.
+// share its blocks of K, if all clusters run at once and it is estimated to be
+// faster. A CTA takes `block` us a block of K and `store` us a row of its part
+// of the tile; joining the parts takes 0.5 us and `join` us a row of the tile
+// with 2 CTAs, 1.7 and 2.8 times that with 4 and 8 (what a CTA reads from the
+// others grows, and distributed shared memory gives it about 10 bytes a cycle).
+// Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 128 x 512 x 2048 12.0 /
+// 12.8 / 13.6 / 16.6 us, 128 x 4096 x 7168 28.0 / 21.1 / 17.8, 1 x 4096 x 7168
+// 32.4 / 19.5 / 12.5 / 17.1 (16 clusters of 8 were asked for and 15 fit).
+struct Costs {
+  float block, join, store, fixed;
+};
+
 template <typename Resident>
-Plan plan(int64_t units, int KB, int rows, float block, float fixed, int sms, Resident resident) {
+Plan plan(int64_t units, int KB, int rows, const Costs& c, int sms, Resident resident) {
   Plan best;
   for (int split = 1; split <= kMaxSplit && split <= KB; split *= 2) {
     if (split > 1 && units > resident(split)) break;
     const float waves = units * split > sms ? (float)units * split / sms : 1.0f;
-    const float us = block * ((KB + split - 1) / split) * waves + (split > 1 ? 0.5f + 0.025f * rows : 0.0f) + fixed;
+    float us = c.block * ((KB + split - 1) / split) * waves + c.store * rows / split + c.fixed;
+    if (split > 1) us += 0.5f + c.join * rows * (split == 2 ? 1.0f : split == 4 ? 1.7f : 2.8f);
     if (split == 1 || us < best.us) best = Plan{split, us};
   }
   return best;
@@ -972,12 +979,11 @@ struct FewLaunch {
     units = tiles_of(p, NT) * p.NB;
     ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, smem);
     if (!ok) return;
-    // 0.22, 0.26 and 0.5 us a block (split 1, 56 blocks: 16.4, 18.8 and 29.1 us)
-    plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, 4.0f, sms,
-                          [&](int split) {
-                            return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3,
-                                                     kFewThreads, smem, split);
-                          });
+    // a block: split 1 of 56 blocks takes 16.4, 18.8 and 29.1 us
+    const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, 0.013f, 0.0f, 4.0f};
+    plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, costs, sms, [&](int split) {
+      return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3, kFewThreads, smem, split);
+    });
   }
   int run(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t ldw, Params& p, void* stream) const {
     CUtensorMap ma, mw;
@@ -1006,7 +1012,9 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
-  Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, 0.5f, 6.0f, sms, [&](int split) {
+  const float store = p.c_unit == 16 ? 0.0f : p.c_unit == 8 ? 0.01f : p.c_unit == 4 ? 0.03f : 0.05f;
+  const Costs costs{0.39f, 0.026f, store, 6.0f};
+  Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, costs, sms, [&](int split) {
     return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, smem, split);
   });
   // Few rows: the other kernel where it is estimated to be faster (64 x 4096 x
