@@ -576,9 +576,33 @@ int fp8_grouped_gemm(const uint8_t* a_codes, const float* a_sf, int64_t M, int64
                      const float* w_sf, const int32_t* offsets, int E, int64_t N, int64_t K, int64_t ldw, void* c,
                      int c_type, int64_t ldc, void* stream);
 
+/* Workspace bytes fp8_moe_forward needs (0 for an unsupported shape). */
+size_t fp8_moe_forward_workspace_size(int64_t T, int64_t K, int64_t I, int E, int k);
+
+/*
+ * fp8_moe_forward -- the expert forward in 8-bit block-scaled form:
+ * moe_route_topk, moe_permute, fp8_quantize into expert order, the gate and up
+ * products (rounded to BF16), fp8_swiglu_quantize, the down product (BF16) and
+ * the weighted sum over each token's experts (moe_unsort_tokens).
+ *   x              (T, K) BF16, leading dimension K.  router_logits (T, E) f32.
+ *   w1_codes       (E, 2I, K) codes, rows [gate 0..I-1 | up 0..I-1], with w1_sf
+ *                  (E, ceil(2I/128), ceil(K/128)); w2_codes (E, K, I) with
+ *                  w2_sf: fp8_quantize_weight's results.
+ *   y              (T, K) BF16.
+ *   ws             >= fp8_moe_forward_workspace_size(T, K, I, E, k) bytes,
+ *                  256-byte aligned.
+ * Requires K % 16 == 0, I % 16 == 0, 1 <= k <= 16, k <= E <= 1024. Nothing is
+ * allocated and nothing waits for the device, so the call can be captured in
+ * a CUDA graph. Errors: INVALID, UNSUPPORTED, WORKSPACE, LAUNCH.
+ */
+int fp8_moe_forward(const void* x, const float* router_logits, int64_t T, int64_t K, int64_t I, int E, int k,
+                    const uint8_t* w1_codes, const float* w1_sf, const uint8_t* w2_codes, const float* w2_sf, void* y,
+                    void* ws, size_t ws_bytes, void* stream);
+
 /* Waits for `stream`, then reads and clears the device status word that the
  * GEMM and fused-front kernels set when a bounded wait runs out (and
- * nvfp4_rmsnorm_rope_quantize sets on a position out of range) (README "Key Lessons" 5: no
+ * nvfp4_rmsnorm_rope_quantize sets on a position, fp8_quantize and the
+ * sorted-token calls on a row, out of range) (README "Key Lessons" 5: no
  * silent failure). Returns NVFP4MOE_OK, NVFP4MOE_ERR_DEVICE_TIMEOUT or
  * NVFP4MOE_ERR_LAUNCH (a CUDA error on the stream). */
 int nvfp4moe_last_device_status(void* stream);

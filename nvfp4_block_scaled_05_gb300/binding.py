@@ -101,6 +101,9 @@ _SIGS = {
                           _i64, _c_void_p]),
     "fp8_grouped_gemm": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _int, _i64, _i64,
                                 _i64, _c_void_p, _int, _i64, _c_void_p]),
+    "fp8_moe_forward_workspace_size": (_size, [_i64, _i64, _i64, _int, _int]),
+    "fp8_moe_forward": (_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _c_void_p, _c_void_p,
+                               _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
     "nvfp4moe_last_device_status": (_int, [_c_void_p]),
     "nvfp4moe_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "nvfp4moe_set_test_stall": (None, [_int]),
@@ -615,6 +618,42 @@ def fp8_grouped_gemm(a_codes, a_sf, w_codes, w_sf, offsets, out=None, out_dtype=
     _check(lib().fp8_grouped_gemm(pa, psa, M, lda, w_codes.data_ptr(), psw, po, E, N, K, K, pc, out_type, ldc,
                                   _stream()), "fp8_grouped_gemm")
     return out
+
+
+def fp8_moe_forward_workspace_size(T, K, I, E, k):
+    return int(lib().fp8_moe_forward_workspace_size(T, K, I, E, k))
+
+
+def prepare_fp8_moe_weights(w1, w2):
+    """w1 (E, 2I, K) rows [gate | up] and w2 (E, K, I) in BF16, F16 or F32 ->
+    the weights fp8_moe_forward takes."""
+    E, two_i, K = w1.shape
+    if two_i % 2 or tuple(w2.shape) != (E, K, two_i // 2):
+        raise NVFP4Error("w1 must be (E, 2I, K) and w2 (E, K, I)")
+    w1_codes, w1_sf = fp8_quantize_weight(w1)
+    w2_codes, w2_sf = fp8_quantize_weight(w2)
+    return {"E": E, "I": two_i // 2, "K": K, "w1_codes": w1_codes, "w1_sf": w1_sf, "w2_codes": w2_codes,
+            "w2_sf": w2_sf}
+
+
+def fp8_moe_forward(x, logits, weights, k, ws=None, y=None):
+    """The whole expert forward in 8-bit block-scaled form; weights from
+    prepare_fp8_moe_weights()."""
+    E, I, K = weights["E"], weights["I"], weights["K"]
+    _dev(x, "x")
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
+        raise NVFP4Error("x must be (T, %d) BF16" % K)
+    T = x.shape[0]
+    pl = _flat(logits, "logits", torch.float32, T * E)
+    if ws is None:
+        ws = torch.empty(fp8_moe_forward_workspace_size(T, K, I, E, k), dtype=torch.uint8, device=x.device)
+    if y is None:
+        y = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
+    _check(lib().fp8_moe_forward(_ptr(x), pl, T, K, I, E, k, _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]),
+                                 _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]),
+                                 _flat(y, "y", torch.bfloat16, T * K), _ptr(ws), ws.numel(), _stream()),
+           "fp8_moe_forward")
+    return y
 
 
 def _c_type(out, out_dtype):

@@ -274,3 +274,82 @@ extern "C" int nvfp4_linear(const uint8_t* a_codes, const uint8_t* a_sf, const f
   return nvfp4_grouped_gemm(a_codes, a_sf, gs_a, a_rows, w_codes, w_sf, gs_w, bounds, 1, N, K, c, ldc,
                             stream);
 }
+
+// ------------------------------------------------------------------ 8-bit expert forward
+
+namespace {
+
+// topk_ids, topk_w, offsets, perm_to_flat, flat_to_perm, a_codes, a_sf, h_codes,
+// h_sf, then gate_up and the experts' outputs in one place (the first is used
+// up when the second is written), then the permute scratch.
+struct Fp8Layout {
+  int64_t off[11];
+  int64_t total;
+};
+
+Fp8Layout fp8_layout(int64_t T, int64_t K, int64_t I, int E, int k) {
+  Fp8Layout L{};
+  const int64_t M = T * k;
+  int64_t o = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = o;
+    o += up256(bytes > 0 ? bytes : 1);
+    return at;
+  };
+  L.off[0] = take(M * 4);
+  L.off[1] = take(M * 4);
+  L.off[2] = take((E + 1) * 4);
+  L.off[3] = take(M * 4);
+  L.off[4] = take(M * 4);
+  L.off[5] = take(M * K);
+  L.off[6] = take(M * ceil_div(K, 128) * 4);
+  L.off[7] = take(M * I);
+  L.off[8] = take(M * ceil_div(I, 128) * 4);
+  L.off[9] = take(M * (2 * I > K ? 2 * I : K) * 2);
+  L.off[10] = take((int64_t)moe_permute_workspace_size(T, k, E));
+  L.total = o;
+  return L;
+}
+
+bool fp8_shape_ok(int64_t T, int64_t K, int64_t I, int E, int k) {
+  return T >= 0 && K > 0 && K % 16 == 0 && K < (1ll << 24) && I > 0 && I % 16 == 0 && I < (1ll << 24) && k >= 1 &&
+         k <= 16 && E >= k && E <= 1024 && T * k < (1ll << 31) - 128;
+}
+
+}  // namespace
+
+extern "C" size_t fp8_moe_forward_workspace_size(int64_t T, int64_t K, int64_t I, int E, int k) {
+  if (!fp8_shape_ok(T, K, I, E, k)) return 0;
+  return (size_t)fp8_layout(T, K, I, E, k).total;
+}
+
+extern "C" int fp8_moe_forward(const void* x, const float* router_logits, int64_t T, int64_t K, int64_t I, int E,
+                               int k, const uint8_t* w1_codes, const float* w1_sf, const uint8_t* w2_codes,
+                               const float* w2_sf, void* y, void* ws, size_t ws_bytes, void* stream) {
+  NVFP4_CHECK(fp8_shape_ok(T, K, I, E, k), NVFP4MOE_ERR_UNSUPPORTED);
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4_CHECK(x && router_logits && w1_codes && w1_sf && w2_codes && w2_sf && y, NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(aligned(x, 16) && aligned(y, 16) && aligned(w1_codes, 16) && aligned(w2_codes, 16), NVFP4MOE_ERR_INVALID);
+  const Fp8Layout L = fp8_layout(T, K, I, E, k);
+  NVFP4_CHECK(ws && ws_bytes >= (size_t)L.total && aligned(ws, 256), NVFP4MOE_ERR_WORKSPACE);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  int32_t* ids = reinterpret_cast<int32_t*>(w + L.off[0]);
+  float* topw = reinterpret_cast<float*>(w + L.off[1]);
+  int32_t* offsets = reinterpret_cast<int32_t*>(w + L.off[2]);
+  int32_t* p2f = reinterpret_cast<int32_t*>(w + L.off[3]);
+  int32_t* f2p = reinterpret_cast<int32_t*>(w + L.off[4]);
+  uint8_t* a_codes = w + L.off[5];
+  float* a_sf = reinterpret_cast<float*>(w + L.off[6]);
+  uint8_t* h_codes = w + L.off[7];
+  float* h_sf = reinterpret_cast<float*>(w + L.off[8]);
+  void* wide = w + L.off[9];
+  const int64_t M = T * k;
+  NVFP4_TRY(moe_route_topk(router_logits, T, E, k, ids, topw, stream));
+  NVFP4_TRY(moe_permute(ids, T, k, E, offsets, p2f, f2p, w + L.off[10], moe_permute_workspace_size(T, k, E), stream));
+  NVFP4_TRY(fp8_quantize(x, NVFP4MOE_BF16, T, K, K, f2p, k, M, a_codes, a_sf, stream));
+  NVFP4_TRY(fp8_grouped_gemm(a_codes, a_sf, M, K, w1_codes, w1_sf, offsets, E, 2 * I, K, K, wide, NVFP4MOE_BF16, 2 * I,
+                             stream));
+  NVFP4_TRY(fp8_swiglu_quantize(wide, NVFP4MOE_BF16, M, I, 2 * I, h_codes, h_sf, stream));
+  NVFP4_TRY(fp8_grouped_gemm(h_codes, h_sf, M, I, w2_codes, w2_sf, offsets, E, K, I, I, wide, NVFP4MOE_BF16, K, stream));
+  return moe_unsort_tokens(wide, NVFP4MOE_BF16, M, K, K, f2p, T, k, topw, y, K, stream);
+}

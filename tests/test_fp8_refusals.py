@@ -67,3 +67,19 @@ def test_sorted_tokens(lib):
     assert back(dx=vp((1 << 20) + 2)) == INVALID
     assert lib.moe_unsort_tokens(P, 0, 8, 10, 9, P, 4, 2, None, P, 10, None) == INVALID
     assert lib.moe_unsort_tokens_backward(P, 0, 4, 10, 10, P, 2, None, P, 10, P, 8, 10, P, None) == INVALID
+
+
+def test_expert_forward(lib):
+    sz = ctypes.c_size_t
+    T, K, I, E, k = 16, 256, 128, 8, 2
+    need = lib.fp8_moe_forward_workspace_size(T, K, I, E, k)
+    assert need > 0
+    for bad in [(T, 200, I, E, k), (T, K, 100, E, k), (T, K, I, 1, 2), (T, K, I, 1025, k), (T, K, I, E, 17), (-1, K, I, E, k)]:
+        assert lib.fp8_moe_forward_workspace_size(*bad) == 0
+
+    def run(x=P, T=T, K=K, w2=P, y=P, ws=P, n=need):
+        return lib.fp8_moe_forward(x, P, T, K, I, E, k, P, P, w2, P, y, ws, sz(n), None)
+    assert run(T=0) == 0
+    assert run(K=200) == UNSUPPORTED
+    assert run(x=None) == INVALID and run(w2=None) == INVALID and run(y=vp((1 << 20) + 8)) == INVALID
+    assert run(n=need - 1) == -3 and run(ws=None) == -3 and run(ws=vp((1 << 20) + 16)) == -3
