@@ -171,6 +171,39 @@ __device__ __forceinline__ void tc_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) 
       : "memory");
 }
 
+// A converged warp's wait on a barrier, as wait_bounded, with one vote to an
+// attempt; the result is the same in all lanes.
+__device__ __forceinline__ bool try_wait_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred p, p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns,
+                                          int* status, int site) {
+  if (__builtin_expect(try_wait_warp(bar, parity), 1)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_warp(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      bool give_up = *abort_flag != 0;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
+        give_up = true;
+        *abort_flag = 1;
+        if (atomicCAS(&status[0], 0, NVFP4MOE_ERR_DEVICE_TIMEOUT) == 0) status[1] = site;
+      }
+      if (__any_sync(0xFFFFFFFFu, give_up)) return false;
+    }
+  }
+}
+
 // Four f32 of another CTA's shared memory (shared::cluster address).
 __device__ __forceinline__ void ld_shared_cluster_v4(uint32_t addr, float* v) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -437,16 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t adesc0 = sdesc_kmajor_sw128(sbase);
     const uint64_t bdesc0 = sdesc_kmajor_sw128(sbase + OFF_B);
     if (p.test_stall && first < total)
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 32));
+      ok = wait_warp(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 32);
     for (int t = first; ok && t < total; t += stride) {
       int e, nb, row0, rows, ncols;
       sch.decode(t, e, nb, row0, rows, ncols);
       const uint32_t idesc = idesc_e4m3(BM, (ncols + 15) / 16 * 16);
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t stage = g % STAGES, buf = g & 1u;
-        ok = wait_bounded(bar_full + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns, p.status, 34) &&
-             wait_bounded(bar_acce + 8 * buf, ((g >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 33);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = wait_warp(bar_full + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns, p.status, 34) &&
+             wait_warp(bar_acce + 8 * buf, ((g >> 1) & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 33);
         if (__builtin_expect(!ok, 0)) break;
         tc_fence_after();
         const uint64_t ad = adesc0 + ((stage * A_BYTES) >> 4);
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k) {
           if (kg + k < kb1) {
             const uint32_t bar = bar_done + 8 * (g % STAGES);
-            ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar, (g / STAGES & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 36));
+            ok = wait_warp(bar, (g / STAGES & 1u) ^ 1u, abort_flag, p.wait_limit_ns, p.status, 36);
             if (!ok) break;
             float* out = scales + (g % kScaleSlots) * (2 * BM) + i;
 #pragma unroll
@@ -537,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < HN; ++i) acc[i] = 0.0f;
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t stage = g % STAGES, buf = g & 1u;
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_done + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns,
-                                                  p.status, 35));
+        ok = wait_warp(bar_done + 8 * stage, g / STAGES & 1u, abort_flag, p.wait_limit_ns, p.status, 35);
         if (__builtin_expect(!ok, 0)) break;
         tc_fence_after();
         const float s = scales[(g % kScaleSlots) * (2 * BM) + half * BM + row];
@@ -736,11 +767,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const uint64_t wdesc0 = sdesc_kmajor_sw128(sbase);
     const uint64_t tdesc0 = sdesc_kmajor_sw128(sbase + C::OFF_T);
     if (p.test_stall && any)
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 42));
+      ok = wait_warp(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 42);
     for (int kb = kb0; ok && kb < kb1; ++kb) {
-      ok = wait_bounded(bar_acce + 8 * buf, bphase, abort_flag, p.wait_limit_ns, p.status, 43) &&
-           wait_bounded(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 44);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = wait_warp(bar_acce + 8 * buf, bphase, abort_flag, p.wait_limit_ns, p.status, 43) &&
+           wait_warp(bar_full + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 44);
       if (!ok) break;
       tc_fence_after();
       const uint64_t wd = wdesc0 + ((stage * C::W_BYTES) >> 4);
@@ -783,7 +813,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           a[h][k] = in && r < rows ? __ldg(sa + (int64_t)r * p.KB + kg + k) * w : 0.0f;
         }
       }
-      if (!wait_bounded(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 46)) break;
+      if (!wait_warp(bar_sfe + 8 * slot, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 46)) break;
 #pragma unroll
       for (int k = 0; k < C::SBLOCKS; ++k)
 #pragma unroll
@@ -807,9 +837,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     for (int kb = kb0; kb < kb1; ++kb) {
       const int in_group = (kb - kb0) % C::SBLOCKS;
       if (in_group == 0)
-        ok = wait_bounded(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 47);
-      ok = ok && wait_bounded(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 45);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = wait_warp(bar_sff + 8 * slot, sphase, abort_flag, p.wait_limit_ns, p.status, 47);
+      ok = ok && wait_warp(bar_done + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 45);
       if (!ok) break;
       tc_fence_after();
       const float4* f = reinterpret_cast<const float4*>(scales + slot * C::SCALE_FLOATS + in_group * NT);
