@@ -161,9 +161,10 @@ def _e4m3(q):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("M,I", [(1, 16), (5, 144), (40, 2048)])
 def test_swiglu_codes_are_those_of_nearby_values(M, I, dtype):
-    """The f32 h is within 2^-21 of the exact one (exp: 2 ulp, the sum, the
-    quotient and the product half an ulp each), so the scale is within 2^-20 and
-    every code between the codes of x * inv * (1 -+ 2^-20)."""
+    """The f32 h is within 2^-20 of the exact one (exponential and reciprocal 2 ulp
+    each, the sum and the products half an ulp, the exponent's own rounding
+    |g| 2^-24 with |g| below 10 wherever the code is not 0), so the scale is too
+    and every code lies between the codes of x * inv * (1 -+ 2^-20)."""
     gu = _rand((M, 2 * I), 7, 2.0, dtype)
     gu[0, :4] = torch.tensor([-100.0, 100.0, 0.0, -20.0]).to(dtype)
     codes, sf = B.fp8_swiglu_quantize(gu.to(DEV))
