@@ -4,7 +4,10 @@ Every function here has the name of the C entry point it calls and only
 marshals arguments: it allocates outputs with torch (device memory is the one
 thing torch is used for), passes raw pointers and torch's current stream, and
 raises on a non-zero status. All arithmetic runs in the library's kernels; if
-the library cannot be loaded, every call fails loudly.
+the library cannot be loaded, every call fails loudly. The calls whose kernels
+take a few microseconds (the sorted tokens, the 8-bit operators) are marshalled
+by the extension module _tensor_calls (csrc/tensor_calls.cpp), the others by
+ctypes.
 """
 import ctypes
 import os
@@ -23,9 +26,6 @@ FRONT_FUSED_QUANTIZE_MAX_ROWS = 32768
 NVFP4MOE_BF16 = 0           # element types
 NVFP4MOE_F16 = 1
 NVFP4MOE_F32 = 2
-
-_TYPES = {torch.bfloat16: NVFP4MOE_BF16, torch.float16: NVFP4MOE_F16, torch.float32: NVFP4MOE_F32}
-_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -130,6 +130,20 @@ def lib():
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+_calls_module = None
+
+
+def _calls():
+    """The extension module of the short calls."""
+    global _calls_module
+    if _calls_module is None:
+        lib()                       # builds what is stale
+        from . import _tensor_calls
+        _tensor_calls.set_error(NVFP4Error)
+        _calls_module = _tensor_calls
+    return _calls_module
 
 
 def _ptr(t):
@@ -414,210 +428,60 @@ def moe_combine(out, topk_w, flat_to_perm, y=None):
 
 # ------------------------------------------------------------------ tokens in expert order
 
-def _rows(t, name, types=_TYPES):
-    """(rows, columns, leading dimension, address) of a 2-D CUDA tensor of one of
-    `types` whose rows are contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise NVFP4Error("%s must be a CUDA tensor" % name)
-    if t.dtype not in types or t.dim() != 2:
-        raise NVFP4Error("%s must be a matrix of one of %s" % (name, ", ".join(str(d) for d in types)))
-    n, c = t.shape
-    ld, step = t.stride()
-    if c > 1 and step != 1 or n > 1 and ld < c:
-        raise NVFP4Error("the rows of %s must be contiguous and must not overlap" % name)
-    return n, c, ld if n > 1 else max(c, ld), t.data_ptr()
-
-
-def _flat(t, name, dtype, numel):
-    """The address of a contiguous CUDA tensor of `numel` elements."""
-    _dev(t, name)
-    if t.dtype != dtype or t.numel() != numel:
-        raise NVFP4Error("%s must have %d elements of %s" % (name, numel, dtype))
-    return t.data_ptr()
-
-
-def _out(t, name, n, c, like, dtype=None):
-    """The caller's (n, c) output, or a new one, with its leading dimension and address."""
-    dtype = dtype or like.dtype
-    if t is None:
-        t = torch.empty((n, c), dtype=dtype, device=like.device)
-        return t, c, t.data_ptr()
-    rows, cols, ld, ptr = _rows(t, name, (dtype,))
-    if rows != n or cols != c:
-        raise NVFP4Error("%s must be %dx%d" % (name, n, c))
-    return t, ld, ptr
-
-
-def _slots(flat_to_perm, k, topk_w):
-    """Tokens, and the addresses of flat_to_perm and topk_w."""
-    _dev(flat_to_perm, "flat_to_perm")
-    n = flat_to_perm.numel()
-    if flat_to_perm.dtype != torch.int32 or k < 1 or n % k:
-        raise NVFP4Error("flat_to_perm must be int32 with k entries a token")
-    return n // k, flat_to_perm.data_ptr(), None if topk_w is None else _flat(topk_w, "topk_w", torch.float32, n)
-
-
-def _dots(t, name, n, c, like, topk_w, T, k):
-    """Leading dimension and address of the operand of the dot products, and the
-    (T, k) gradient of the weights with its address."""
-    if t is None:
-        return 0, None, None, None
-    rows, cols, ld, ptr = _rows(t, name, (like.dtype,))
-    if rows != n or cols != c or topk_w is None:
-        raise NVFP4Error("%s must be %dx%d, given together with topk_w" % (name, n, c))
-    d_w = torch.empty((T, k), dtype=torch.float32, device=like.device)
-    return ld, ptr, d_w, d_w.data_ptr()
-
-
 def moe_sort_tokens(x, flat_to_perm, k, topk_w=None, n_rows=None, rows=None):
     """x (T, K) in expert order: rows[flat_to_perm[t*k+j]] = topk_w[t, j] * x[t]
     (n_rows rows, T*k if not given; those that no entry names are not written)."""
-    T, K, ldx, px = _rows(x, "x")
-    tokens, pf, pw = _slots(flat_to_perm, k, topk_w)
-    if tokens != T:
-        raise NVFP4Error("flat_to_perm must have k entries for each row of x")
-    if n_rows is None:
-        n_rows = T * k if rows is None else rows.shape[0]
-    rows, ldr, pr = _out(rows, "rows", n_rows, K, x)
-    _check(lib().moe_sort_tokens(px, _TYPES[x.dtype], T, K, ldx, pf, k, pw, pr, n_rows, ldr, _stream()),
-           "moe_sort_tokens")
-    return rows
+    return _calls().moe_sort_tokens(x, flat_to_perm, k, topk_w, n_rows, rows)
 
 
 def moe_sort_tokens_backward(d_rows, flat_to_perm, k, topk_w=None, x=None, dx=None):
     """The gradients of moe_sort_tokens: (dx, d_w); d_w is computed when x (and
     topk_w) is given, else None."""
-    n_rows, K, ldr, pr = _rows(d_rows, "d_rows")
-    T, pf, pw = _slots(flat_to_perm, k, topk_w)
-    ldx, px, d_w, pd = _dots(x, "x", T, K, d_rows, topk_w, T, k)
-    dx, lddx, po = _out(dx, "dx", T, K, d_rows)
-    _check(lib().moe_sort_tokens_backward(pr, _TYPES[d_rows.dtype], n_rows, K, ldr, pf, T, k, pw, px, ldx, po, lddx,
-                                          pd, _stream()), "moe_sort_tokens_backward")
-    return dx, d_w
+    return _calls().moe_sort_tokens_backward(d_rows, flat_to_perm, k, topk_w, x, dx)
 
 
 def moe_unsort_tokens(rows, flat_to_perm, k, topk_w=None, y=None):
     """y[t] = sum_j topk_w[t, j] * rows[flat_to_perm[t*k+j]]."""
-    n_rows, K, ldr, pr = _rows(rows, "rows")
-    T, pf, pw = _slots(flat_to_perm, k, topk_w)
-    y, ldy, py = _out(y, "y", T, K, rows)
-    _check(lib().moe_unsort_tokens(pr, _TYPES[rows.dtype], n_rows, K, ldr, pf, T, k, pw, py, ldy, _stream()),
-           "moe_unsort_tokens")
-    return y
+    return _calls().moe_unsort_tokens(rows, flat_to_perm, k, topk_w, y)
 
 
 def moe_unsort_tokens_backward(dy, flat_to_perm, k, topk_w=None, rows=None, n_rows=None, d_rows=None):
     """The gradients of moe_unsort_tokens: (d_rows, d_w); d_w is computed when
     rows (and topk_w) is given, else None. Rows that no entry of flat_to_perm
     names are not written."""
-    T, K, ldy, py = _rows(dy, "dy")
-    tokens, pf, pw = _slots(flat_to_perm, k, topk_w)
-    if tokens != T:
-        raise NVFP4Error("flat_to_perm must have k entries for each row of dy")
-    if n_rows is None:
-        n_rows = rows.shape[0] if rows is not None else d_rows.shape[0] if d_rows is not None else T * k
-    ldr, pr, d_w, pd = _dots(rows, "rows", n_rows, K, dy, topk_w, T, k)
-    d_rows, lddr, po = _out(d_rows, "d_rows", n_rows, K, dy)
-    _check(lib().moe_unsort_tokens_backward(py, _TYPES[dy.dtype], T, K, ldy, pf, k, pw, pr, ldr, po, n_rows, lddr, pd,
-                                            _stream()), "moe_unsort_tokens_backward")
-    return d_rows, d_w
+    return _calls().moe_unsort_tokens_backward(dy, flat_to_perm, k, topk_w, rows, n_rows, d_rows)
 
 
 # ------------------------------------------------------------------ 8-bit block-scaled operands
-
-def _blocks(n):
-    return (n + 127) // 128
-
-
-def _codes_and_scales(codes, sf, n, K, device):
-    """The caller's codes and scales of n rows, or new ones, with their addresses."""
-    kb = _blocks(K)
-    if codes is None:
-        codes = torch.empty((n, K), dtype=torch.uint8, device=device)
-    else:
-        _flat(codes, "codes", torch.uint8, n * K)
-    if sf is None:
-        sf = torch.empty((n, kb), dtype=torch.float32, device=device)
-    else:
-        _flat(sf, "sf", torch.float32, n * kb)
-    return codes, sf, codes.data_ptr(), sf.data_ptr()
-
 
 def fp8_quantize(x, flat_to_perm=None, k=1, out_rows=None, codes=None, sf=None):
     """(rows, K) BF16, F16 or F32 -> E4M3 codes (uint8) and one f32 scale per row
     and 128 elements. With flat_to_perm, row r is written to the k rows
     flat_to_perm[r*k .. r*k+k) of the out_rows (rows*k if not given) output rows."""
-    M, K, ldx, px = _rows(x, "x")
-    pf = None
-    if flat_to_perm is not None:
-        n, pf, _ = _slots(flat_to_perm, k, None)
-        if n != M:
-            raise NVFP4Error("flat_to_perm must have k entries for each row of x")
-    if out_rows is None:
-        out_rows = M if flat_to_perm is None else M * k
-    codes, sf, pc, ps = _codes_and_scales(codes, sf, out_rows, K, x.device)
-    _check(lib().fp8_quantize(px, _TYPES[x.dtype], M, K, ldx, pf, k, out_rows, pc, ps, _stream()), "fp8_quantize")
-    return codes, sf
+    return _calls().fp8_quantize(x, flat_to_perm, k, out_rows, codes, sf)
 
 
 def fp8_swiglu_quantize(gate_up, codes=None, sf=None):
     """Rows [gate | up] (rows, 2I) -> codes and scales of silu(gate) * up."""
-    M, two_i, ld, px = _rows(gate_up, "gate_up")
-    if two_i % 2:
-        raise NVFP4Error("gate_up must have as many up as gate columns")
-    codes, sf, pc, ps = _codes_and_scales(codes, sf, M, two_i // 2, gate_up.device)
-    _check(lib().fp8_swiglu_quantize(px, _TYPES[gate_up.dtype], M, two_i // 2, ld, pc, ps, _stream()),
-           "fp8_swiglu_quantize")
-    return codes, sf
+    return _calls().fp8_swiglu_quantize(gate_up, codes, sf)
 
 
 def fp8_quantize_weight(w):
     """(N, K) or (E, N, K) weights -> codes of the same shape and one f32 scale
     per 128 x 128 block, (ceil(N/128), ceil(K/128)) or with E in front."""
-    _dev(w, "w")
-    if w.dtype not in _TYPES or w.dim() not in (2, 3):
-        raise NVFP4Error("w must be (N, K) or (E, N, K) in BF16, F16 or F32")
-    N, K = w.shape[-2:]
-    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    sf = torch.empty((*w.shape[:-2], _blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
-    _check(lib().fp8_quantize_weight(_ptr(w), _TYPES[w.dtype], 1 if w.dim() == 2 else w.shape[0], N, K, K,
-                                     _ptr(codes), _ptr(sf), _stream()), "fp8_quantize_weight")
-    return codes, sf
+    return _calls().fp8_quantize_weight(w)
 
 
 def fp8_linear(a_codes, a_sf, w_codes, w_sf, out=None, out_dtype=torch.bfloat16):
     """A (M, K) x W (N, K) -> C (M, N): codes uint8 or float8_e4m3fn, scales f32
     as fp8_quantize and fp8_quantize_weight give them."""
-    M, K, lda, pa = _rows(a_codes, "a_codes", _CODES)
-    N, wk, ldw, pw = _rows(w_codes, "w_codes", _CODES)
-    if wk != K:
-        raise NVFP4Error("a_codes and w_codes must have the same K")
-    kb = _blocks(K)
-    psa = _flat(a_sf, "a_sf", torch.float32, M * kb)
-    psw = _flat(w_sf, "w_sf", torch.float32, _blocks(N) * kb)
-    dtype, out_type = _c_type(out, out_dtype)
-    out, ldc, pc = _out(out, "out", M, N, a_codes, dtype)
-    _check(lib().fp8_linear(pa, psa, M, lda, pw, psw, N, K, ldw, pc, out_type, ldc, _stream()), "fp8_linear")
-    return out
+    return _calls().fp8_linear(a_codes, a_sf, w_codes, w_sf, out, out_dtype)
 
 
 def fp8_grouped_gemm(a_codes, a_sf, w_codes, w_sf, offsets, out=None, out_dtype=torch.bfloat16):
     """A (M, K), rows grouped by expert (compact rows, offsets (E + 1) int32), x
     W (E, N, K) -> C (M, N)."""
-    M, K, lda, pa = _rows(a_codes, "a_codes", _CODES)
-    _dev(w_codes, "w_codes")
-    if w_codes.dtype not in _CODES or w_codes.dim() != 3 or w_codes.shape[2] != K:
-        raise NVFP4Error("w_codes must be (E, N, K) codes with the K of a_codes")
-    E, N = w_codes.shape[:2]
-    kb = _blocks(K)
-    psa = _flat(a_sf, "a_sf", torch.float32, M * kb)
-    psw = _flat(w_sf, "w_sf", torch.float32, E * _blocks(N) * kb)
-    po = _flat(offsets, "offsets", torch.int32, E + 1)
-    dtype, out_type = _c_type(out, out_dtype)
-    out, ldc, pc = _out(out, "out", M, N, a_codes, dtype)
-    _check(lib().fp8_grouped_gemm(pa, psa, M, lda, w_codes.data_ptr(), psw, po, E, N, K, K, pc, out_type, ldc,
-                                  _stream()), "fp8_grouped_gemm")
-    return out
+    return _calls().fp8_grouped_gemm(a_codes, a_sf, w_codes, w_sf, offsets, out, out_dtype)
 
 
 def fp8_moe_forward_workspace_size(T, K, I, E, k):
@@ -644,23 +508,17 @@ def fp8_moe_forward(x, logits, weights, k, ws=None, y=None):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
         raise NVFP4Error("x must be (T, %d) BF16" % K)
     T = x.shape[0]
-    pl = _flat(logits, "logits", torch.float32, T * E)
+    for t, name, dtype, shape in ((logits, "logits", torch.float32, (T, E)), (y, "y", torch.bfloat16, (T, K))):
+        if t is not None and (_dev(t, name).dtype != dtype or tuple(t.shape) != shape):
+            raise NVFP4Error("%s must be %dx%d of %s" % (name, *shape, dtype))
     if ws is None:
         ws = torch.empty(fp8_moe_forward_workspace_size(T, K, I, E, k), dtype=torch.uint8, device=x.device)
     if y is None:
         y = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
-    _check(lib().fp8_moe_forward(_ptr(x), pl, T, K, I, E, k, _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]),
-                                 _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]),
-                                 _flat(y, "y", torch.bfloat16, T * K), _ptr(ws), ws.numel(), _stream()),
-           "fp8_moe_forward")
+    _check(lib().fp8_moe_forward(_ptr(x), _ptr(logits), T, K, I, E, k, _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]),
+                                 _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]), _ptr(y), _ptr(ws), ws.numel(),
+                                 _stream()), "fp8_moe_forward")
     return y
-
-
-def _c_type(out, out_dtype):
-    dtype = out_dtype if out is None else out.dtype
-    if dtype not in _TYPES:
-        raise NVFP4Error("the result must be one of %s" % ", ".join(str(d) for d in _TYPES))
-    return dtype, _TYPES[dtype]
 
 
 # ------------------------------------------------------------------ the forward
