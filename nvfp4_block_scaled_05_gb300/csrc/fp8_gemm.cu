@@ -1056,7 +1056,7 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   } else if (rows <= 32) {
     const FewLaunch<32> f(p, sms);
     if (f.ok && f.plan.us <= tiles.us) return f.run(a_codes, lda, w_codes, ldw, p, stream);
-  } else if (rows <= 64) {
+  } else if (tiles_of(p, 64) * p.NB <= 4 * sms) {
     const FewLaunch<64> f(p, sms);
     if (f.ok && f.plan.us <= tiles.us) return f.run(a_codes, lda, w_codes, ldw, p, stream);
   }

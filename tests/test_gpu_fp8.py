@@ -213,7 +213,8 @@ def _check(got, a, sa, w, sw, out, what):
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 4096, 7168), (2, 128, 128), (17, 100, 144), (128, 256, 512),
-                                   (129, 257, 528), (333, 1111, 2000), (64, 640, 16), (700, 384, 1040)])
+                                   (129, 257, 528), (333, 1111, 2000), (64, 640, 16), (700, 384, 1040),
+                                   (24, 384, 640), (40, 333, 400), (16, 130, 7168), (32, 129, 2064)])
 def test_linear(M, N, K, out):
     a, sa, w, sw = _operands(M, 1, N, K, M + N + K)
     got = B.fp8_linear(a, sa, w[0], sw[0], out_dtype=out)
@@ -222,9 +223,23 @@ def test_linear(M, N, K, out):
     assert torch.equal(B.fp8_linear(a.view(F8), sa, w[0].view(F8), sw[0], out_dtype=out), got)   # and again
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1200, 2304, 1040), (1300, 2303, 528), (1150, 2306, 144), (1290, 2308, 256),
+                                   (128, 4096, 7168), (100, 4100, 7168), (65, 8200, 1024), (4100, 300, 400)])
+def test_linear_of_many_tiles(M, N, K, out):
+    """More tiles than SMs, or tiles whose blocks of K a cluster shares; rows of C
+    that are whole sectors, whole 16, 8, 4 bytes, or none of them."""
+    a, sa, w, sw = _operands(M, 1, N, K, M + N + K)
+    got = B.fp8_linear(a, sa, w[0], sw[0], out_dtype=out)
+    _check(got, a, sa, w[0], sw[0], out, "linear")
+    assert B.nvfp4moe_last_device_status() == 0
+
+
 @pytest.mark.parametrize("counts,N,K", [([1], 128, 128), ([0, 0, 5], 200, 272), ([3, 0, 128, 129, 0, 1], 257, 400),
                                         ([0, 300, 16, 17, 32, 33, 64, 65], 512, 1024),
-                                        ([2] * 70, 384, 256), ([1000, 0, 0, 1], 300, 2000)])
+                                        ([2] * 70, 384, 256), ([1000, 0, 0, 1], 300, 2000),
+                                        ([900, 0, 700, 1, 300, 129], 2050, 400), ([1500, 127, 0, 600], 2304, 528),
+                                        ([1] * 600, 520, 128)])
 def test_grouped(counts, N, K):
     E, M = len(counts), sum(counts)
     a, sa, w, sw = _operands(M, E, N, K, M + N)
@@ -310,9 +325,9 @@ def test_empty_products():
     assert (out == 2).all()
 
 
-@pytest.mark.parametrize("M", [3, 700])
-def test_a_wait_that_runs_out_is_reported(M):
-    a, sa, w, sw = _operands(M, 1, 512, 1024, 8)
+@pytest.mark.parametrize("M,N", [(3, 512), (700, 512), (2500, 4096), (128, 4096)])
+def test_a_wait_that_runs_out_is_reported(M, N):
+    a, sa, w, sw = _operands(M, 1, N, 1024, 8)
     good = B.fp8_linear(a, sa, w[0], sw[0])
     assert B.nvfp4moe_last_device_status() == 0
     try:
