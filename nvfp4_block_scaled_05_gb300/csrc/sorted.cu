@@ -48,11 +48,62 @@ template <> struct Elem<float> {
   static __device__ __forceinline__ float put(float v) { return v; }
 };
 
-// V consecutive elements as one access (V * sizeof(T) is 16 bytes, or V is 1).
+// V consecutive elements: 16 bytes where all rows start on 16-byte boundaries,
+// else two elements, of which rows of an odd width hold every other one's pairs
+// unaligned (the same for all lanes of a warp).
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   T e[V];
 };
+
+// What is read for a pack: nothing but loads, so that those of all of a token's
+// rows are in flight before the first is used. A pair of 16-bit elements comes
+// from the two 4-byte words at and after it (one element before the pair to two
+// behind it: columns [kHead, K - kTail) are read in pairs, the others one by
+// one), a pair of f32 from two loads.
+template <int V> constexpr int kHead = V > 2 ? 0 : 2;
+template <int V> constexpr int kTail = V > 2 ? 0 : 2;
+
+template <typename T, int V>
+struct Raw {
+  Pack<T, V> v;
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V > 2) {
+      v = *reinterpret_cast<const Pack<T, V>*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v.e[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ Pack<T, V> get(const T*) const { return v; }
+};
+
+template <typename T>
+struct Words {
+  uint32_t w0, w1;
+  __device__ __forceinline__ void load(const T* p) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3));
+    w0 = w[0];
+    w1 = w[1];
+  }
+  __device__ __forceinline__ Pack<T, 2> get(const T* p) const {
+    const uint32_t both = __funnelshift_r(w0, w1, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8);
+    return *reinterpret_cast<const Pack<T, 2>*>(&both);
+  }
+};
+template <> struct Raw<__nv_bfloat16, 2> : Words<__nv_bfloat16> {};
+template <> struct Raw<__half, 2> : Words<__half> {};
+
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v) {
+  using P = Pack<T, V>;
+  if (V > 2 || reinterpret_cast<uintptr_t>(p) % sizeof(P) == 0) {
+    *reinterpret_cast<P*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = v.e[i];
+  }
+}
 
 // The rows of a token's k slots (-1 for a slot without one) and its weights.
 // A row outside [0, n_rows) is an error of the caller's: recorded, and taken
@@ -102,34 +153,37 @@ __global__ void __launch_bounds__(NT) spread_kernel(const Args a) {
   float dot[KM];
 #pragma unroll
   for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
-  const int64_t whole = a.K / V * V;
+  const int64_t head = kHead<V>, whole = a.K >= head + kTail<V> + V ? head + (a.K - head - kTail<V>) / V * V : 0;
   // the block's share of the columns (all of them with dots)
   const int part = kDot ? 0 : blockIdx.y, parts = kDot ? 1 : gridDim.y;
-  for (int64_t c = (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
+  for (int64_t c = head + (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
     using P = Pack<T, V>;
-    const P x = *reinterpret_cast<const P*>(src + c);
-    P o[KM];
+    Raw<T, V> xr, o[KM];
+    xr.load(src + c);
     if constexpr (kDot) {
 #pragma unroll
       for (int j = 0; j < KM; ++j)
         if (j < a.k && row[j] >= 0)
-          o[j] = *reinterpret_cast<const P*>(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
+          o[j].load(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
     }
+    const P x = xr.get(src + c);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
       if (j < a.k && row[j] >= 0) {
-        P y;
+        P y, d;
+        if constexpr (kDot) d = o[j].get(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float v = Elem<T>::get(x.e[i]);
           y.e[i] = Elem<T>::put(wt[j] * v);
-          if constexpr (kDot) dot[j] = fmaf(v, Elem<T>::get(o[j].e[i]), dot[j]);
+          if constexpr (kDot) dot[j] = fmaf(v, Elem<T>::get(d.e[i]), dot[j]);
         }
-        *reinterpret_cast<P*>(static_cast<T*>(a.rows_out) + row[j] * a.ldr_out + c) = y;
+        store_pack<T, V>(static_cast<T*>(a.rows_out) + row[j] * a.ldr_out + c, y);
       }
     }
   }
-  for (int64_t c = whole + part * NT + threadIdx.x; c < a.K; c += parts * NT) {   // after the last whole pack
+  for (int64_t i = part * NT + threadIdx.x; i < a.K - (whole > 0 ? whole - head : 0); i += parts * NT) {   // the other columns
+    const int64_t c = whole > 0 && i >= head ? whole + i - head : i;
     const float v = Elem<T>::get(src[c]);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
@@ -156,25 +210,30 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
   float dot[KM];
 #pragma unroll
   for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
-  const int64_t whole = a.K / V * V;
+  const int64_t head = kHead<V>, whole = a.K >= head + kTail<V> + V ? head + (a.K - head - kTail<V>) / V * V : 0;
   // the block's share of the columns (all of them with dots)
   const int part = kDot ? 0 : blockIdx.y, parts = kDot ? 1 : gridDim.y;
-  for (int64_t c = (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
+  for (int64_t c = head + (part * NT + threadIdx.x) * V; c < whole; c += parts * NT * V) {
     using P = Pack<T, V>;
-    P r[KM], x;
+    Raw<T, V> r[KM], xr;
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-      if (j < a.k && row[j] >= 0) r[j] = *reinterpret_cast<const P*>(rows + row[j] * a.ldr_in + c);
-    if constexpr (kDot) x = *reinterpret_cast<const P*>(tok + c);
+      if (j < a.k && row[j] >= 0) r[j].load(rows + row[j] * a.ldr_in + c);
+    P x;
+    if constexpr (kDot) {
+      xr.load(tok + c);
+      x = xr.get(tok + c);
+    }
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
       if (j < a.k && row[j] >= 0) {
+        const P d = r[j].get(rows + row[j] * a.ldr_in + c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float v = Elem<T>::get(r[j].e[i]);
+          const float v = Elem<T>::get(d.e[i]);
           acc[i] = fmaf(wt[j], v, acc[i]);
           if constexpr (kDot) dot[j] = fmaf(Elem<T>::get(x.e[i]), v, dot[j]);
         }
@@ -183,9 +242,10 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
     P y;
 #pragma unroll
     for (int i = 0; i < V; ++i) y.e[i] = Elem<T>::put(acc[i]);
-    *reinterpret_cast<P*>(out + c) = y;
+    store_pack<T, V>(out + c, y);
   }
-  for (int64_t c = whole + part * NT + threadIdx.x; c < a.K; c += parts * NT) {
+  for (int64_t i = part * NT + threadIdx.x; i < a.K - (whole > 0 ? whole - head : 0); i += parts * NT) {
+    const int64_t c = whole > 0 && i >= head ? whole + i - head : i;
     float acc = 0.0f;
     const float x = kDot ? Elem<T>::get(tok[c]) : 0.0f;
 #pragma unroll
@@ -201,42 +261,52 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
   if constexpr (kDot) store_dots<NT, KM>(a, t, dot, row);
 }
 
-template <typename T, int V, int KM, int NT>
-void launch_nt(const Args& a, bool spread, bool dot, int parts, cudaStream_t s) {
+template <typename T, int V, int KM, int NT, bool kSpread, bool kDot>
+void launch_nt(const Args& a, int parts, cudaStream_t s) {
   const dim3 grid((unsigned)a.T, (unsigned)parts);
-  if (spread) {
-    if (dot) spread_kernel<T, V, KM, NT, true><<<grid, NT, 0, s>>>(a);
-    else spread_kernel<T, V, KM, NT, false><<<grid, NT, 0, s>>>(a);
-  } else {
-    if (dot) collect_kernel<T, V, KM, NT, true><<<grid, NT, 0, s>>>(a);
-    else collect_kernel<T, V, KM, NT, false><<<grid, NT, 0, s>>>(a);
-  }
+  if constexpr (kSpread) spread_kernel<T, V, KM, NT, kDot><<<grid, NT, 0, s>>>(a);
+  else collect_kernel<T, V, KM, NT, kDot><<<grid, NT, 0, s>>>(a);
 }
 
-// Blocks of 64 threads for the sums and the dot products: more blocks in
-// different phases to an SM (loads, stores, reduction), 8192 x 7168 BF16, k = 8:
-// sum 163 us against 187 with 256 threads, spread with dots 322 against 477,
-// sum with dots 184 against 215. The plain spread is better with 256 (162
-// against 176). With few tokens the columns of a token are divided over blocks,
-// or, where a block has to see all of them for its dot products, its 256
-// threads see them in fewer rounds (128 tokens: 6.1 against 11.9; from four
-// tokens an SM on, 608: 38.6 against 31.9).
+// Blocks of 64 threads for the sums and the dot products (128 for pairs of
+// 16-bit elements, which take more rounds): more blocks in different phases to
+// an SM (loads, stores, reduction). 8192 x 7168 BF16, k = 8: sum 163 us against
+// 187 with 256 threads, spread with dots 322 against 477, sum with dots 184
+// against 215; pairs, 4096 x 7166: spread with dots 242 against 269 with 64. The
+// plain spread is better with 256 (162 against 176). With few tokens the columns
+// of a token are divided over blocks, or, where a block has to see all of them
+// for its dot products, its 256 threads (512 for many pairs: 32 x 7167 BF16 9.5
+// us against 11.2) see them in fewer rounds (128 tokens: 6.1 against 11.9; from
+// four tokens an SM on, 608: 38.6 against 31.9).
 template <typename T, int V, int KM>
 void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
+  constexpr int NT = V == 2 && sizeof(T) == 2 ? 128 : 64;
   const int64_t sms = device_num_sms();
   const int64_t packs = ceil_div(a.K, V);
   auto parts = [&](int threads, int64_t blocks) {
     const int64_t most = ceil_div(packs, threads), want = ceil_div(blocks, a.T);
     return (int)(most < want ? (most > 0 ? most : 1) : want);
   };
-  if (dot ? a.T < 4 * sms : spread)
-    launch_nt<T, V, KM, 256>(a, spread, dot, dot ? 1 : parts(256, 4 * sms), s);
-  else
-    launch_nt<T, V, KM, 64>(a, spread, dot, dot ? 1 : parts(64, 16 * sms), s);
+  if (!dot) {
+    if (spread) launch_nt<T, V, KM, 256, true, false>(a, parts(256, 4 * sms), s);
+    else launch_nt<T, V, KM, NT, false, false>(a, parts(NT, 16 * sms), s);
+  } else if (V == 2 && KM <= 8 && a.T < sms && packs >= 2048) {
+    if constexpr (V == 2 && KM <= 8) {
+      if (spread) launch_nt<T, V, KM, 512, true, true>(a, 1, s);
+      else launch_nt<T, V, KM, 512, false, true>(a, 1, s);
+    }
+  } else if (a.T < 4 * sms) {
+    if (spread) launch_nt<T, V, KM, 256, true, true>(a, 1, s);
+    else launch_nt<T, V, KM, 256, false, true>(a, 1, s);
+  } else {
+    if (spread) launch_nt<T, V, KM, NT, true, true>(a, 1, s);
+    else launch_nt<T, V, KM, NT, false, true>(a, 1, s);
+  }
 }
 
 // 16-byte accesses where every row of every operand starts on a 16-byte
-// boundary, single elements otherwise.
+// boundary, pairs of elements otherwise (4096 x 7167 BF16, k = 8, sum: 131 us
+// against 166 with single elements; 4096 x 7168: 88).
 template <typename T>
 void launch_t(const Args& a, bool spread, bool dot, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
@@ -248,9 +318,9 @@ void launch_t(const Args& a, bool spread, bool dot, cudaStream_t s) {
     else if (a.k <= 8) launch_v<T, V, 8>(a, spread, dot, s);
     else launch_v<T, V, 16>(a, spread, dot, s);
   } else {
-    if (a.k <= 4) launch_v<T, 1, 4>(a, spread, dot, s);
-    else if (a.k <= 8) launch_v<T, 1, 8>(a, spread, dot, s);
-    else launch_v<T, 1, 16>(a, spread, dot, s);
+    if (a.k <= 4) launch_v<T, 2, 4>(a, spread, dot, s);
+    else if (a.k <= 8) launch_v<T, 2, 8>(a, spread, dot, s);
+    else launch_v<T, 2, 16>(a, spread, dot, s);
   }
 }
 
@@ -266,7 +336,8 @@ int launch(Args& a, int type, bool spread, bool dot, void* stream) {
 
 int check_sizes(int type, int64_t T, int64_t K, int k, int64_t n_rows) {
   NVFP4_CHECK(type == NVFP4MOE_BF16 || type == NVFP4MOE_F16 || type == NVFP4MOE_F32, NVFP4MOE_ERR_UNSUPPORTED);
-  NVFP4_CHECK(T >= 0 && K >= 0 && k >= 1 && k <= kMaxK && n_rows >= 0 && T < (1ll << 31) && T * k < (1ll << 31),
+  NVFP4_CHECK(T >= 0 && K >= 0 && K < (1ll << 30) && k >= 1 && k <= kMaxK && n_rows >= 0 && T < (1ll << 31) &&
+                  T * k < (1ll << 31),
               NVFP4MOE_ERR_UNSUPPORTED);
   return NVFP4MOE_OK;
 }
