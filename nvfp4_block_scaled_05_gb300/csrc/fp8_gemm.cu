@@ -204,11 +204,17 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// Four f32 of another CTA's shared memory (shared::cluster address).
+// Four f32 from and into the shared memory of a CTA of the cluster
+// (shared::cluster address).
 __device__ __forceinline__ void ld_shared_cluster_v4(uint32_t addr, float* v) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3])
                : "memory");
 }
 
@@ -321,23 +327,43 @@ __device__ __forceinline__ void store_tile(T* c, int64_t ldc, const float (&acc)
   }
 }
 
-// C's rows [row0, row0 + rows), columns [col0, col0 + ncols) from the partial
-// sums of `split` CTAs (rows of TN f32, part_bytes apart, at the same place in
-// the shared memory of each): eight columns of a row by one thread, added in
-// the order of the blocks of K.
-template <typename T, int TN>
-__device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int part_bytes, int rank, int split,
-                                           int row0, int rows, int col0, int ncols, int threads) {
-  for (int i = rank * threads + threadIdx.x; i < rows * (TN / 8); i += split * threads) {
+// The parts of a tile's sums, one from each of the `split` CTAs of a cluster
+// that share its blocks of K. Row r of the tile is joined by CTA r / per, which
+// adds the parts in the order of the blocks. Where a thread holds a row (the
+// 128-row tiles), every CTA stores its part of it straight into the owner's
+// shared memory, at slot `rank` (kPull false); where a thread holds a column
+// (few rows), whose stores would be four bytes each, the parts stay with the
+// CTAs that made them and the owner reads them there (kPull). Measured, 128 x
+// 512 x 2048 as two 128-row tiles in 2, 4 and 8 parts: 12.7, 12.6 and 12.8 us,
+// read by the owner 12.8, 13.6 and 16.6; few rows, 333 x 1111 x 2000 in 2
+// parts: 9.5 us, stored by the makers 11.9.
+struct Parts {
+  uint32_t base;   // shared memory of this CTA
+  int pitch;       // bytes of a staged row
+  int per;         // rows that one CTA joins
+  int rank, split;
+  // where this CTA's part of a row goes that is joined by its owner
+  __device__ __forceinline__ uint32_t slot(int row) const {
+    return mapa_shared(base + (rank * per + row % per) * pitch, row / per);
+  }
+};
+
+// C's rows [row0, row0 + rows), columns [col0, col0 + ncols) of those that this
+// CTA joins: eight columns of a row by one thread, the parts all on their way
+// at once (a remote load takes about a microsecond).
+template <typename T, int TN, bool kPull>
+__device__ __forceinline__ void join_parts(const Params& p, const Parts& parts, int row0, int rows, int col0, int ncols,
+                                           int threads) {
+  const int first = parts.rank * parts.per, mine = min(parts.per, rows - first);
+  for (int i = threadIdx.x; i < mine * (TN / 8); i += threads) {
     const int row = i / (TN / 8), col = i % (TN / 8) * 8;
     if (col >= ncols) continue;
-    // all parts are on their way at once: a remote load takes about a microsecond
     float w[kMaxSplit][8], v[8];
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r) {
-      if (r < split) {
-        const uint32_t own = sbase + row * part_bytes + col * 4;
-        const uint32_t from = split > 1 ? mapa_shared(own, r) : own;
+      if (r < parts.split) {
+        const uint32_t at = parts.base + (kPull ? first + row : r * parts.per + row) * parts.pitch + col * 4;
+        const uint32_t from = kPull && parts.split > 1 ? mapa_shared(at, r) : at;
         ld_shared_cluster_v4(from, w[r]);
         ld_shared_cluster_v4(from + 16, w[r] + 4);
       }
@@ -347,9 +373,9 @@ __device__ __forceinline__ void join_parts(const Params& p, uint32_t sbase, int 
       v[k] = w[0][k];
 #pragma unroll
       for (int r = 1; r < kMaxSplit; ++r)
-        if (r < split) v[k] += w[r][k];
+        if (r < parts.split) v[k] += w[r][k];
     }
-    store8(static_cast<T*>(p.c) + (int64_t)(row0 + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_unit);
+    store8(static_cast<T*>(p.c) + (int64_t)(row0 + first + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_unit);
   }
 }
 
@@ -591,13 +617,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
         }
       }
+      // (a cluster has one tile: its rings are free for the parts once all of
+      // its CTAs' products are read)
+      if (split > 1) cluster_sync_all();
       if (!ok || !live) continue;
-      if (split > 1) {   // this CTA's part of the sums, for the join below
-        if (row >= rows) continue;
-        float4* part = reinterpret_cast<float4*>(smem + row * kPartBytes) + col0 / 4;
+      if (split > 1) {
+        if (row < rows) {
+          const Parts parts{sbase, kPartBytes, (rows + split - 1) / split, rank, split};
+          const uint32_t part = parts.slot(row) + col0 * 4;
 #pragma unroll
-        for (int i = 0; i < HN / 4; ++i)
-          part[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+          for (int i = 0; i < HN; i += 4) st_shared_cluster_v4(part + 4 * i, acc + i);
+        }
         continue;
       }
       T* out = static_cast<T*>(p.c) + (int64_t)(row0 + quad * 32) * p.ldc + nb * BN + col0;
@@ -612,17 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (split > 1) {
-    // The cluster's CTAs have each summed their blocks of K of one tile; eight
-    // columns of a row are joined by one thread, in the order of the blocks.
-    // Every CTA's part stays in shared memory until all have read it.
     __syncwarp();
-    cluster_sync_all();
+    if (warp < kEpiWarp0) cluster_sync_all();   // the epilogue's, above
+    cluster_sync_all();                         // all parts are where they are joined
     int e, nb, row0, rows, ncols;
     sch.decode(first, e, nb, row0, rows, ncols);
-    join_parts<T, BN>(p, sbase, kPartBytes, rank, split, row0, rows, nb * BN, ncols, kThreads);
-    __syncwarp();
-    cluster_sync_all();
+    join_parts<T, BN, false>(p, Parts{sbase, kPartBytes, (rows + split - 1) / split, rank, split}, row0, rows, nb * BN,
+                             ncols, kThreads);
   }
+
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -695,12 +723,44 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   int32_t* tile_start = start + 2 * p.E;
   const Sched sch{start, tile_start, p.E, p.NB, p.N, NT, 128};
 
-  if (tid == 0) {
-    prefetch_tensormap(&tm_a);
-    prefetch_tensormap(&tm_w);
+  const int split = p.split;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int unit = (int)blockIdx.x / split;
+  int e = 0, nb = 0, row0 = 0, rows = 0, ncols = 0, kb0 = 0, kb1 = 0;
+  auto blocks_of_k = [&]() {
+    kb0 = p.KB * rank / split;
+    kb1 = p.KB * (rank + 1) / split;
+  };
+  if (!p.offsets) {   // one group: the tile needs no schedule
+    const int mt = (p.M + NT - 1) / NT;
+    nb = unit / mt;
+    row0 = (unit - nb * mt) * NT;
+    rows = min(NT, p.M - row0);
+    ncols = min(128, p.N - nb * 128);
+    blocks_of_k();
+  } else {
+    load_groups(p, start);
   }
-  load_groups(p, start);
-  if (tid == 32) {
+  // the producer's state (thread 0)
+  uint32_t p_stage = 0, p_phase = 0, filled = 0, fill_phase = 0;
+  int p_kb = kb0;
+  auto fill = [&]() {   // the next block of K into the next stage
+    const uint32_t full = bar_full + 8 * p_stage;
+    mbar_arrive_expect_tx(full, C::W_BYTES + C::T_BYTES);
+    tma_load_2d(sbase + p_stage * C::W_BYTES, &tm_w, full, p_kb * BK, e * p.N + nb * 128,
+                p.w_once ? l2_policy_evict_first() : l2_policy_evict_normal());
+    tma_load_2d(sbase + C::OFF_T + p_stage * C::T_BYTES, &tm_a, full, p_kb * BK, row0, l2_policy_evict_last());
+    filled |= 1u << p_stage;
+    fill_phase = (fill_phase & ~(1u << p_stage)) | (p_phase << p_stage);
+    ++p_kb;
+    if (++p_stage == STAGES) {
+      p_stage = 0;
+      p_phase ^= 1;
+    }
+  };
+  if (tid == 0) {
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_a);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_done + 8 * s, 1);
@@ -714,47 +774,36 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     mbar_init(bar_never, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // one group: the first loads are on their way while the rest is set up
+    for (int i = 0; i < STAGES && p_kb < kb1; ++i) fill();
   }
   if (warp == 1) {
     __syncwarp();
     tmem_alloc(smem_addr(tmem_slot), C::TMEM);
     tmem_relinquish();
   }
-  __syncthreads();
-  if (warp == 0) scan_tiles(sch, tile_start);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int split = p.split;
-  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
-  const int unit = (int)blockIdx.x / split;
-  const bool any = unit < tile_start[p.E];   // the same for every CTA of a cluster
-  int e = 0, nb = 0, row0 = 0, rows = 0, ncols = 0;
-  if (any) sch.decode(unit, e, nb, row0, rows, ncols);
-  const int kb0 = p.KB * rank / split, kb1 = any ? p.KB * (rank + 1) / split : kb0;
+  if (p.offsets) {
+    if (warp == 0) scan_tiles(sch, tile_start);
+    __syncthreads();
+    if (unit < tile_start[p.E]) {   // the same for every CTA of a cluster
+      sch.decode(unit, e, nb, row0, rows, ncols);
+      blocks_of_k();
+      p_kb = kb0;
+    }
+  }
+  const bool any = rows > 0;
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- producer
-    const uint64_t pol_w = p.w_once ? l2_policy_evict_first() : l2_policy_evict_normal();
-    const uint64_t pol_a = l2_policy_evict_last();
-    uint32_t stage = 0, phase = 0, filled = 0, fill_phase = 0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!wait_bounded(bar_done + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 41)) {
-        ok = false;
-        break;
-      }
-      const uint32_t full = bar_full + 8 * stage;
-      mbar_arrive_expect_tx(full, C::W_BYTES + C::T_BYTES);
-      tma_load_2d(sbase + stage * C::W_BYTES, &tm_w, full, kb * BK, e * p.N + nb * 128, pol_w);
-      tma_load_2d(sbase + C::OFF_T + stage * C::T_BYTES, &tm_a, full, kb * BK, row0, pol_a);
-      filled |= 1u << stage;
-      fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
+    while (ok && p_kb < kb1) {
+      ok = wait_bounded(bar_done + 8 * p_stage, p_phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 41);
+      if (ok) fill();
     }
     if (!ok)   // copies still in flight complete before the CTA may exit
       for (int s = 0; s < STAGES; ++s)
@@ -877,22 +926,22 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (ok) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        if (i < rows)
-          *reinterpret_cast<float*>(smem + i * C::PART_BYTES + (quad * 32 + lane) * 4) = acc[i];
+        if (i < rows) *reinterpret_cast<float*>(smem + i * C::PART_BYTES + (quad * 32 + lane) * 4) = acc[i];
     }
   }
 
   __syncwarp();
   if (split > 1) cluster_sync_all();
   else __syncthreads();
+  const Parts parts{sbase, C::PART_BYTES, rows > split ? (rows + split - 1) / split : 1, rank, split};
   if (p.c_type == NVFP4MOE_BF16)
-    join_parts<__nv_bfloat16, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+    join_parts<__nv_bfloat16, 128, true>(p, parts, row0, rows, nb * 128, ncols, kFewThreads);
   else if (p.c_type == NVFP4MOE_F16)
-    join_parts<__half, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+    join_parts<__half, 128, true>(p, parts, row0, rows, nb * 128, ncols, kFewThreads);
   else
-    join_parts<float, 128>(p, sbase, C::PART_BYTES, rank, split, row0, rows, nb * 128, ncols, kFewThreads);
+    join_parts<float, 128, true>(p, parts, row0, rows, nb * 128, ncols, kFewThreads);
   __syncwarp();
-  if (split > 1) cluster_sync_all();
+  if (split > 1) cluster_sync_all();   // every CTA's part stays until all have read it
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -961,14 +1010,13 @@ struct Plan {
 // Where there are few tiles, each goes to a cluster of 2, 4 or 8 CTAs that
 // share its blocks of K, if all clusters run at once and it is estimated to be
 // faster. A CTA takes `block` us a block of K and `store` us a row of its part
-// of the tile; joining the parts takes 0.5 us and `join` us a row of the tile
-// with 2 CTAs, 1.7 and 2.8 times that with 4 and 8 (what a CTA reads from the
-// others grows, and distributed shared memory gives it about 10 bytes a cycle).
-// Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 128 x 512 x 2048 12.0 /
-// 12.8 / 13.6 / 16.6 us, 128 x 4096 x 7168 28.0 / 21.1 / 17.8, 1 x 4096 x 7168
-// 32.4 / 19.5 / 12.5 / 17.1 (16 clusters of 8 were asked for and 15 fit).
+// of the tile; joining the parts takes 0.5 us and join[0 .. 2] us a row of the
+// tile with 2, 4 and 8 CTAs (distributed shared memory moves about 10 bytes a
+// cycle and SM). Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 128 x 512 x
+// 2048 12.0 / 12.7 / 12.6 / 12.8 us, 128 x 4096 x 7168 27.6 / 20.7 / 16.9, 1 x
+// 4096 x 7168 26.1 / 16.3 / 11.0 (15 clusters of 8 fit, and 16 would be needed).
 struct Costs {
-  float block, join, store, fixed;
+  float block, join[3], store, fixed;
 };
 
 template <typename Resident>
@@ -978,7 +1026,7 @@ Plan plan(int64_t units, int KB, int rows, const Costs& c, int sms, Resident res
     if (split > 1 && units > resident(split)) break;
     const float waves = units * split > sms ? (float)units * split / sms : 1.0f;
     float us = c.block * ((KB + split - 1) / split) * waves + c.store * rows / split + c.fixed;
-    if (split > 1) us += 0.5f + c.join * rows * (split == 2 ? 1.0f : split == 4 ? 1.7f : 2.8f);
+    if (split > 1) us += 0.5f + c.join[split == 2 ? 0 : split == 4 ? 1 : 2] * rows;
     if (split == 1 || us < best.us) best = Plan{split, us};
   }
   return best;
@@ -1009,7 +1057,7 @@ struct FewLaunch {
     ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, smem);
     if (!ok) return;
     // a block: split 1 of 56 blocks takes 16.4, 18.8 and 29.1 us
-    const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, 0.013f, 0.0f, 4.0f};
+    const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, {0.013f, 0.022f, 0.037f}, 0.0f, 4.0f};
     plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, costs, sms, [&](int split) {
       return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3, kFewThreads, smem, split);
     });
@@ -1042,7 +1090,7 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
   const float store = p.c_unit == 16 ? 0.0f : p.c_unit == 8 ? 0.01f : p.c_unit == 4 ? 0.03f : 0.05f;
-  const Costs costs{0.39f, 0.026f, store, 6.0f};
+  const Costs costs{0.39f, {0.026f, 0.038f, 0.043f}, store, 6.0f};
   Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, costs, sms, [&](int split) {
     return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, smem, split);
   });
