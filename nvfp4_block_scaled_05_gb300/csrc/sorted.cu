@@ -273,11 +273,18 @@ void launch_nt(const Args& a, int parts, cudaStream_t s) {
 // an SM (loads, stores, reduction). 8192 x 7168 BF16, k = 8: sum 163 us against
 // 187 with 256 threads, spread with dots 322 against 477, sum with dots 184
 // against 215; pairs, 4096 x 7166: spread with dots 242 against 269 with 64. The
-// plain spread is better with 256 (162 against 176). With few tokens the columns
-// of a token are divided over blocks, or, where a block has to see all of them
-// for its dot products, its 256 threads (512 for many pairs: 32 x 7167 BF16 9.5
-// us against 11.2) see them in fewer rounds (128 tokens: 6.1 against 11.9; from
-// four tokens an SM on, 608: 38.6 against 31.9).
+// plain spread is better with 256 (162 against 176). Short rows leave threads of
+// such blocks idle, so they get a warp (forward and backward of weighted rows, 8192
+// tokens, k = 8, with a warp / 64, or 128 for pairs: 64 columns 18.2 / 26.0 us, 401
+// 56.6 / 63.7, 1024 84.1 / 88.1), and the middle of the range 64 threads in the plain
+// spread; spread and sum of 8192 BF16 tokens, k = 8, with a warp / 64 (the sum
+// of pairs 128) / 256 threads for the spread: 64 columns 12.6 / 14.6 / 26.0 us,
+// 401 (201 pairs) 40.5 / 44.7 / 46.6, 500 (250 pairs) 49.4 / 47.9 / 51.4, 2048 (256
+// pieces of 16 bytes) 106.0 / 104.5 / 105.1. With few tokens the columns of a
+// token are divided over blocks, or, where a block has to see all of them for
+// its dot products, its 256 threads (512 for many pairs: 32 x 7167 BF16 9.5 us
+// against 11.2) see them in fewer rounds (128 tokens: 6.1 against 11.9; from four
+// tokens an SM on, 608: 38.6 against 31.9).
 template <typename T, int V, int KM>
 void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
   constexpr int NT = V == 2 && sizeof(T) == 2 ? 128 : 64;
@@ -288,8 +295,16 @@ void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
     return (int)(most < want ? (most > 0 ? most : 1) : want);
   };
   if (!dot) {
-    if (spread) launch_nt<T, V, KM, 256, true, false>(a, parts(256, 4 * sms), s);
-    else launch_nt<T, V, KM, NT, false, false>(a, parts(NT, 16 * sms), s);
+    if (packs <= 224) {
+      if (spread) launch_nt<T, V, KM, 32, true, false>(a, parts(32, 16 * sms), s);
+      else launch_nt<T, V, KM, 32, false, false>(a, parts(32, 16 * sms), s);
+    } else if (!spread) {
+      launch_nt<T, V, KM, NT, false, false>(a, parts(NT, 16 * sms), s);
+    } else if (packs < 512) {
+      launch_nt<T, V, KM, 64, true, false>(a, parts(64, 16 * sms), s);
+    } else {
+      launch_nt<T, V, KM, 256, true, false>(a, parts(256, 4 * sms), s);
+    }
   } else if (V == 2 && KM <= 8 && a.T < sms && packs >= 2048) {
     if constexpr (V == 2 && KM <= 8) {
       if (spread) launch_nt<T, V, KM, 512, true, true>(a, 1, s);
@@ -298,6 +313,9 @@ void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
   } else if (a.T < 4 * sms) {
     if (spread) launch_nt<T, V, KM, 256, true, true>(a, 1, s);
     else launch_nt<T, V, KM, 256, false, true>(a, 1, s);
+  } else if (packs <= 224) {
+    if (spread) launch_nt<T, V, KM, 32, true, true>(a, 1, s);
+    else launch_nt<T, V, KM, 32, false, true>(a, 1, s);
   } else {
     if (spread) launch_nt<T, V, KM, NT, true, true>(a, 1, s);
     else launch_nt<T, V, KM, NT, false, true>(a, 1, s);

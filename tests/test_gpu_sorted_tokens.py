@@ -61,6 +61,10 @@ CASES = [
     (130, 8, 7168, 0, 0.0, 0, 0),
     (17, 9, 515, 5, 0.5, 0, 3),
     (3, 3, 40, 0, 1.0, 0, 0),           # every slot dropped
+    (700, 8, 401, 9, 0.1, 0, 0),        # many tokens, short rows
+    (700, 2, 72, 0, 0.0, 8, 0),
+    (650, 16, 500, 0, 0.1, 1, 1),
+    (700, 3, 1790, 0, 0.0, 2, 0),
 ]
 
 
