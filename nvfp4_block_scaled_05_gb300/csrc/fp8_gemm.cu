@@ -282,16 +282,21 @@ __device__ __forceinline__ void store8(T* out, const float (&f)[8], int n, int u
   else store_units<uint16_t>(out, v, n);
 }
 
-// One unit from shared to global memory.
+// A warp's staged rows to global memory, in units of sizeof(U).
 template <typename U>
 __device__ __forceinline__ void copy_out(uint8_t* c, int64_t ld_bytes, const uint8_t* staged, int rows, int bytes,
                                          int lane) {
-  constexpr int PER_ROW = kOutRow / sizeof(U);
+  constexpr int PER_ROW = kOutRow / sizeof(U);   // units; 32 / PER_ROW rows at a time
+  const int r = lane / PER_ROW, b = lane % PER_ROW * (int)sizeof(U);
+  c += r * ld_bytes + b;
+  staged += r * kOutPitch + b;
+  const int left = b < bytes ? rows - r : 0;
+  const int64_t step = 32 / PER_ROW * ld_bytes;
 #pragma unroll 8
   for (int i = 0; i < PER_ROW; ++i) {
-    const int u = i * 32 + lane, r = u / PER_ROW, b = u % PER_ROW * (int)sizeof(U);
-    if (r < rows && b < bytes)
-      *reinterpret_cast<U*>(c + r * ld_bytes + b) = *reinterpret_cast<const U*>(staged + r * kOutPitch + b);
+    if (i * (32 / PER_ROW) < left) *reinterpret_cast<U*>(c) = *reinterpret_cast<const U*>(staged);
+    c += step;
+    staged += 32 / PER_ROW * kOutPitch;
   }
 }
 
