@@ -45,13 +45,10 @@ constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK;         // 16 KB
 constexpr int B_BYTES = BN * BK;         // 32 KB
 constexpr int kScaleSlots = 8;           // blocks of K whose factors are in shared memory (see bar_done)
-constexpr int kOutRow = 32;              // bytes of a row of C that an epilogue warp stages at a time,
-constexpr int kOutPitch = kOutRow + 16;  // and their distance (16 bytes against bank conflicts)
 constexpr int OFF_B = STAGES * A_BYTES;
 constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
 constexpr int OFF_SCALE = OFF_BAR + 256;                       // [slot][half][row]
-constexpr int OFF_OUT = OFF_SCALE + kScaleSlots * 2 * BM * 4;  // 32 staged rows of each epilogue warp
-constexpr int OFF_MISC = OFF_OUT + 8 * 32 * kOutPitch;
+constexpr int OFF_MISC = OFF_SCALE + kScaleSlots * 2 * BM * 4;
 constexpr int OFF_SCHED = OFF_MISC + 64;
 constexpr uint32_t TMEM_COLS = 512;      // two buffers of 256 columns
 constexpr int kPartBytes = BN * 4 + 16;  // a row of partial sums in shared memory; 16 bytes against bank conflicts
@@ -212,6 +209,11 @@ __device__ __forceinline__ void ld_shared_cluster_v4(uint32_t addr, float* v) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, const float* v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3])
@@ -282,53 +284,80 @@ __device__ __forceinline__ void store8(T* out, const float (&f)[8], int n, int u
   else store_units<uint16_t>(out, v, n);
 }
 
-// A warp's staged rows to global memory, in units of sizeof(U).
-template <typename U>
-__device__ __forceinline__ void copy_out(uint8_t* c, int64_t ld_bytes, const uint8_t* staged, int rows, int bytes,
-                                         int lane) {
-  constexpr int PER_ROW = kOutRow / sizeof(U);   // units; 32 / PER_ROW rows at a time
-  const int r = lane / PER_ROW, b = lane % PER_ROW * (int)sizeof(U);
-  c += r * ld_bytes + b;
-  staged += r * kOutPitch + b;
-  const int left = b < bytes ? rows - r : 0;
-  const int64_t step = 32 / PER_ROW * ld_bytes;
-#pragma unroll 8
-  for (int i = 0; i < PER_ROW; ++i) {
-    if (i * (32 / PER_ROW) < left) *reinterpret_cast<U*>(c) = *reinterpret_cast<const U*>(staged);
-    c += step;
-    staged += 32 / PER_ROW * kOutPitch;
-  }
+// w[i] = w[i + N] where `on`, for a lane each.
+template <int N, int W>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[W], bool on) {
+#pragma unroll
+  for (int i = 0; i + N < W; ++i) w[i] = on ? w[i + N] : w[i];
 }
 
-// A warp's 32 rows x HN columns of C, of which `rows` and `cols` exist, where
-// the rows of C are not whole 32-byte sectors; lane r holds row r. Its own
-// stores would be an element each, to 32 rows at a time (4096 x 4095 x 2048
-// took 183 us, 4096 x 4096 x 2048 41), so 32 bytes of each row at a time go
-// through shared memory and leave as pieces of rows.
+// The first n values of a row to out, which is aligned to an element only. A
+// store for each would touch 32 rows at a time (4096 x 4095 x 2048, BF16, took
+// 183 us; rows passed on in 32-byte pieces through shared memory 54; this 41.5;
+// 4096 columns and store_row 39.7), so the row leaves in whole sectors: 2, 4, 8
+// and 16 bytes as they are needed to reach a 32-byte boundary, then whole
+// sectors of the values moved down by as many registers, and the rest in 16, 8,
+// 4 and 2 bytes. (Where fewer bytes are left than a step stores, the steps end
+// and they are the rest.)
 template <typename T>
-__device__ __forceinline__ void store_tile(T* c, int64_t ldc, const float (&acc)[HN], int rows, int cols, int unit,
-                                           uint8_t* staged, int lane) {
-  constexpr int N = kOutRow / (int)sizeof(T);   // columns at a time
+__device__ __forceinline__ void store_row_shifted(T* out, const float (&acc)[HN], int n) {
+  constexpr int W = HN * (int)sizeof(T) / 4;
+  uint32_t w[W];
+  uint8_t* c = reinterpret_cast<uint8_t*>(out);
+  int left = n * (int)sizeof(T);
 #pragma unroll
-  for (int p = 0; p < HN / N; ++p) {
-    if (p * N < cols) {   // the whole warp
+  for (int i = 0; i < W; ++i) {
+    if constexpr (sizeof(T) == 2) w[i] = pack2(out, acc[2 * i], acc[2 * i + 1]);
+    else w[i] = __float_as_uint(acc[i]);
+  }
+  auto step = [&](int bytes) {
+    const bool on = (reinterpret_cast<uintptr_t>(c) & bytes) && left >= bytes;
+    c += on ? bytes : 0;
+    left -= on ? bytes : 0;
+    return on;
+  };
+  if constexpr (sizeof(T) == 2) {
+    const bool on = step(2);
+    if (on) *reinterpret_cast<uint16_t*>(c - 2) = (uint16_t)w[0];
+    const uint32_t sel = on ? 0x5432 : 0x3210;
 #pragma unroll
-      for (int q = 0; q < kOutRow / 16; ++q) {
-        alignas(16) T v[16 / sizeof(T)];
+    for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], w[i + 1 < W ? i + 1 : i], sel);
+  }
+  uint32_t t[8];   // the first, then the last words, less than a sector
 #pragma unroll
-        for (int i = 0; i < 16 / (int)sizeof(T); ++i) put(v + i, acc[p * N + q * (16 / (int)sizeof(T)) + i]);
-        *reinterpret_cast<uint4*>(staged + lane * kOutPitch + 16 * q) = *reinterpret_cast<const uint4*>(v);
-      }
-      __syncwarp();
-      uint8_t* out = reinterpret_cast<uint8_t*>(c + p * N);
-      const int64_t ld = ldc * (int64_t)sizeof(T);
-      const int bytes = min(N, cols - p * N) * (int)sizeof(T);
-      if (unit == 16) copy_out<uint4>(out, ld, staged, rows, bytes, lane);
-      else if (unit == 8) copy_out<uint2>(out, ld, staged, rows, bytes, lane);
-      else if (unit == 4) copy_out<uint32_t>(out, ld, staged, rows, bytes, lane);
-      else copy_out<uint16_t>(out, ld, staged, rows, bytes, lane);
-      __syncwarp();
-    }
+  for (int i = 0; i < 8; ++i) t[i] = w[i];
+  const bool on1 = step(4);
+  if (on1) *reinterpret_cast<uint32_t*>(c - 4) = t[0];
+  shift_words<1>(t, on1);
+  const bool on2 = step(8);
+  if (on2) *reinterpret_cast<uint2*>(c - 8) = make_uint2(t[0], t[1]);
+  shift_words<2>(t, on2);
+  const bool on4 = step(16);
+  if (on4) *reinterpret_cast<uint4*>(c - 16) = make_uint4(t[0], t[1], t[2], t[3]);
+#pragma unroll
+  for (int j = 0; j < W / 8; ++j) {
+    uint32_t v[15];   // moved eight at a time: all at once would need registers for them twice
+#pragma unroll
+    for (int i = 0; i < 15; ++i) v[i] = 8 * j + i < W ? w[8 * j + i] : 0;
+    shift_words<4>(v, on4);
+    shift_words<2>(v, on2);
+    shift_words<1>(v, on1);
+    if (left >= 32 * (j + 1)) st_global_32B_stream(c + 32 * j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = left >= 32 * j ? v[i] : t[i];
+  }
+  c += left & ~31;
+  if (left & 16) *reinterpret_cast<uint4*>(c) = make_uint4(t[0], t[1], t[2], t[3]);
+  shift_words<4>(t, left & 16);
+  c += left & 16;
+  if (left & 8) *reinterpret_cast<uint2*>(c) = make_uint2(t[0], t[1]);
+  shift_words<2>(t, left & 8);
+  c += left & 8;
+  if (left & 4) *reinterpret_cast<uint32_t*>(c) = t[0];
+  shift_words<1>(t, left & 4);
+  if constexpr (sizeof(T) == 2) {
+    c += left & 4;
+    if (left & 2) *reinterpret_cast<uint16_t*>(c) = (uint16_t)t[0];
   }
 }
 
@@ -355,22 +384,31 @@ struct Parts {
 
 // C's rows [row0, row0 + rows), columns [col0, col0 + ncols) of those that this
 // CTA joins: eight columns of a row by one thread, the parts all on their way
-// at once (a remote load takes about a microsecond).
+// at once (a remote load takes about a microsecond). Pulled, the eight are
+// neighbours, for few remote loads. Where the parts are here they are TN / 8
+// apart, so that a warp's stores are neighbours at any alignment (500 x 1023 x
+// 7168, f32: 17.2 us against 20.2; x 1024 17.2 against 17.8).
 template <typename T, int TN, bool kPull>
 __device__ __forceinline__ void join_parts(const Params& p, const Parts& parts, int row0, int rows, int col0, int ncols,
                                            int threads) {
+  constexpr int STEP = kPull ? 1 : TN / 8;
   const int first = parts.rank * parts.per, mine = min(parts.per, rows - first);
   for (int i = threadIdx.x; i < mine * (TN / 8); i += threads) {
-    const int row = i / (TN / 8), col = i % (TN / 8) * 8;
+    const int row = i / (TN / 8), col = i % (TN / 8) * (kPull ? 8 : 1);
     if (col >= ncols) continue;
     float w[kMaxSplit][8], v[8];
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r) {
       if (r < parts.split) {
         const uint32_t at = parts.base + (kPull ? first + row : r * parts.per + row) * parts.pitch + col * 4;
-        const uint32_t from = kPull && parts.split > 1 ? mapa_shared(at, r) : at;
-        ld_shared_cluster_v4(from, w[r]);
-        ld_shared_cluster_v4(from + 16, w[r] + 4);
+        if constexpr (kPull) {
+          const uint32_t from = parts.split > 1 ? mapa_shared(at, r) : at;
+          ld_shared_cluster_v4(from, w[r]);
+          ld_shared_cluster_v4(from + 16, w[r] + 4);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[r][k] = ld_shared_f32(at + 4 * STEP * k);
+        }
       }
     }
 #pragma unroll
@@ -380,7 +418,14 @@ __device__ __forceinline__ void join_parts(const Params& p, const Parts& parts, 
       for (int r = 1; r < kMaxSplit; ++r)
         if (r < parts.split) v[k] += w[r][k];
     }
-    store8(static_cast<T*>(p.c) + (int64_t)(row0 + first + row) * p.ldc + col0 + col, v, min(8, ncols - col), p.c_unit);
+    T* out = static_cast<T*>(p.c) + (int64_t)(row0 + first + row) * p.ldc + col0 + col;
+    if constexpr (kPull) {
+      store8(out, v, min(8, ncols - col), p.c_unit);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + STEP * k < ncols) put(out + STEP * k, v[k]);
+    }
   }
 }
 
@@ -637,11 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       T* out = static_cast<T*>(p.c) + (int64_t)(row0 + quad * 32) * p.ldc + nb * BN + col0;
       const int n = min(HN, ncols - col0);
-      if constexpr (kWhole) {
-        if (row < rows) store_row(out + lane * p.ldc, acc, n);
-      } else {
-        store_tile(out, p.ldc, acc, min(32, rows - quad * 32), n, p.c_unit,
-                   smem + OFF_OUT + (warp - kEpiWarp0) * 32 * kOutPitch, lane);
+      if (row < rows) {
+        if constexpr (kWhole) store_row(out + lane * p.ldc, acc, n);
+        else store_row_shifted(out + lane * p.ldc, acc, n);
       }
     }
   }
@@ -1014,14 +1057,13 @@ struct Plan {
 
 // Where there are few tiles, each goes to a cluster of 2, 4 or 8 CTAs that
 // share its blocks of K, if all clusters run at once and it is estimated to be
-// faster. A CTA takes `block` us a block of K and `store` us a row of its part
-// of the tile; joining the parts takes 0.5 us and join[0 .. 2] us a row of the
-// tile with 2, 4 and 8 CTAs (distributed shared memory moves about 10 bytes a
-// cycle and SM). Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 128 x 512 x
+// faster. A CTA takes `block` us a block of K; joining the parts takes 0.5 us and
+// join[0 .. 2] us a row of the tile with 2, 4 and 8 CTAs (distributed shared
+// memory moves about 10 bytes a cycle and SM). Measured, split 1 / 2 / 4 / 8 of the 128-row tiles: 128 x 512 x
 // 2048 12.0 / 12.7 / 12.6 / 12.8 us, 128 x 4096 x 7168 27.6 / 20.7 / 16.9, 1 x
 // 4096 x 7168 26.1 / 16.3 / 11.0 (15 clusters of 8 fit, and 16 would be needed).
 struct Costs {
-  float block, join[3], store, fixed;
+  float block, join[3], fixed;
 };
 
 template <typename Resident>
@@ -1030,7 +1072,7 @@ Plan plan(int64_t units, int KB, int rows, const Costs& c, int sms, Resident res
   for (int split = 1; split <= kMaxSplit && split <= KB; split *= 2) {
     if (split > 1 && units > resident(split)) break;
     const float waves = units * split > sms ? (float)units * split / sms : 1.0f;
-    float us = c.block * ((KB + split - 1) / split) * waves + c.store * rows / split + c.fixed;
+    float us = c.block * ((KB + split - 1) / split) * waves + c.fixed;
     if (split > 1) us += 0.5f + c.join[split == 2 ? 0 : split == 4 ? 1 : 2] * rows;
     if (split == 1 || us < best.us) best = Plan{split, us};
   }
@@ -1062,7 +1104,7 @@ struct FewLaunch {
     ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, smem);
     if (!ok) return;
     // a block: split 1 of 56 blocks takes 16.4, 18.8 and 29.1 us
-    const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, {0.013f, 0.022f, 0.037f}, 0.0f, 4.0f};
+    const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, {0.013f, 0.022f, 0.037f}, 4.0f};
     plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, costs, sms, [&](int split) {
       return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3, kFewThreads, smem, split);
     });
@@ -1094,8 +1136,7 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
-  const float store = p.c_unit == 16 ? 0.0f : p.c_unit == 8 ? 0.01f : p.c_unit == 4 ? 0.03f : 0.05f;
-  const Costs costs{0.39f, {0.026f, 0.038f, 0.043f}, store, 6.0f};
+  const Costs costs{0.39f, {0.026f, 0.038f, 0.043f}, 6.0f};
   Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, costs, sms, [&](int split) {
     return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, smem, split);
   });
