@@ -329,6 +329,13 @@ __device__ __forceinline__ void st_global_32B_stream(void* p, uint32_t a0, uint3
                : "memory");
 }
 
+// 32-byte global store that leaves no line in L1.
+__device__ __forceinline__ void st_global_32B_no_l1(void* p, const uint32_t* w) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 8-byte global store marked as streaming (evict first).
 __device__ __forceinline__ void st_global_8B_stream(void* p, uint32_t a0, uint32_t a1) {
   asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(a0), "r"(a1) : "memory");

@@ -232,35 +232,60 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// The first n of 16 values to out, which is 32-byte aligned.
+// Chunk j (a sector) of a row in registers, as it is stored.
 template <typename T>
-__device__ __forceinline__ void store16(T* out, const float* v, int n) {
-  if (n >= 16) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[8];
+__device__ __forceinline__ void pack_sector(const T* type, const float (&acc)[HN], int j, uint32_t (&w)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack2(out, v[2 * i], v[2 * i + 1]);
-      st_global_32B_stream(out, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        st_global_32B_stream(out + 8 * h, __float_as_uint(v[8 * h]), __float_as_uint(v[8 * h + 1]),
-                             __float_as_uint(v[8 * h + 2]), __float_as_uint(v[8 * h + 3]),
-                             __float_as_uint(v[8 * h + 4]), __float_as_uint(v[8 * h + 5]),
-                             __float_as_uint(v[8 * h + 6]), __float_as_uint(v[8 * h + 7]));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) put(out + i, v[i]);
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 2) w[i] = pack2(type, acc[16 * j + 2 * i], acc[16 * j + 2 * i + 1]);
+    else w[i] = __float_as_uint(acc[8 * j + i]);
   }
 }
 
+// Lane r's row r of a warp's 32 rows, of which `rows` exist, to c + r ldc, which
+// is 32-byte aligned; n columns. All lanes call it. Lanes swap sectors in pairs,
+// so that a store writes 64 bytes of 16 rows and not 32 of 32, and nothing stays
+// in L1 (the tile's stores take as long as three blocks of K, in which nothing is
+// added up). 65536 x 7168 x 2048 in 32 groups, BF16: 820 us; without the swap 841,
+// streaming stores that L1 keeps 874, without the stores 711. In fours, 128 bytes
+// of 8 rows: at best another 10 us, and twice the shuffles.
 template <typename T>
-__device__ __forceinline__ void store_row(T* out, const float (&acc)[HN], int n) {
+__device__ __forceinline__ void store_rows(T* c, int64_t ldc, const float (&acc)[HN], int rows, int n, int lane) {
+  constexpr int PER = 32 / (int)sizeof(T);
+  const bool odd = lane & 1;
+  if (n == HN) {
+    T* even_row = c + (lane & ~1) * ldc + (odd ? PER : 0);
+    T* odd_row = even_row + ldc;
+    const bool even_in = (lane & ~1) < rows, odd_in = (lane | 1) < rows;
 #pragma unroll
-  for (int j = 0; j < HN / 16; ++j)
-    if (16 * j < n) store16(out + 16 * j, acc + 16 * j, n - 16 * j);
+    for (int j = 0; j < HN / PER; j += 2) {
+      uint32_t a[8], b[8];
+      pack_sector(c, acc, j, a);
+      pack_sector(c, acc, j + 1, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a[i] : b[i], 1);
+        a[i] = odd ? got : a[i];
+        b[i] = odd ? b[i] : got;
+      }
+      if (even_in) st_global_32B_no_l1(even_row + PER * j, a);
+      if (odd_in) st_global_32B_no_l1(odd_row + PER * j, b);
+    }
+  } else if (lane < rows) {
+#pragma unroll
+    for (int j = 0; j < HN / PER; ++j) {
+      T* out = c + lane * ldc + PER * j;
+      if (PER * (j + 1) <= n) {
+        uint32_t w[8];
+        pack_sector(c, acc, j, w);
+        st_global_32B_no_l1(out, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (PER * j + i < n) put(out + i, acc[PER * j + i]);
+      }
+    }
+  }
 }
 
 // Eight values of a row of C from column `col` of `ncols` on, in the units that
@@ -293,8 +318,8 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[W], bool on) {
 
 // The first n values of a row to out, which is aligned to an element only. A
 // store for each would touch 32 rows at a time (4096 x 4095 x 2048, BF16, took
-// 183 us; rows passed on in 32-byte pieces through shared memory 54; this 41.5;
-// 4096 columns and store_row 39.7), so the row leaves in whole sectors: 2, 4, 8
+// 183 us; rows passed on in 32-byte pieces through shared memory 54; this 39.3;
+// 4096 columns and store_rows 37), so the row leaves in whole sectors: 2, 4, 8
 // and 16 bytes as they are needed to reach a 32-byte boundary, then whole
 // sectors of the values moved down by as many registers, and the rest in 16, 8,
 // 4 and 2 bytes. (Where fewer bytes are left than a step stores, the steps end
@@ -342,7 +367,7 @@ __device__ __forceinline__ void store_row_shifted(T* out, const float (&acc)[HN]
     shift_words<4>(v, on4);
     shift_words<2>(v, on2);
     shift_words<1>(v, on1);
-    if (left >= 32 * (j + 1)) st_global_32B_stream(c + 32 * j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+    if (left >= 32 * (j + 1)) st_global_32B_no_l1(c + 32 * j, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = left >= 32 * j ? v[i] : t[i];
   }
@@ -682,10 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       T* out = static_cast<T*>(p.c) + (int64_t)(row0 + quad * 32) * p.ldc + nb * BN + col0;
       const int n = min(HN, ncols - col0);
-      if (row < rows) {
-        if constexpr (kWhole) store_row(out + lane * p.ldc, acc, n);
-        else store_row_shifted(out + lane * p.ldc, acc, n);
-      }
+      if constexpr (kWhole) store_rows(out, p.ldc, acc, rows - quad * 32, n, lane);
+      else if (row < rows) store_row_shifted(out + lane * p.ldc, acc, n);
     }
   }
 
