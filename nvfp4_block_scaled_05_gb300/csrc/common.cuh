@@ -47,8 +47,9 @@ int test_stall_on();   // failure-path test hook (nvfp4moe_set_test_stall)
 // Tensor map (defined with the GEMM) of `rows` rows of row_bytes bytes,
 // ld_bytes apart (a multiple of 16): a box of 128 bytes x box_rows rows with
 // the 128-byte swizzle; bytes past a row's end and past the last row read 0.
+// l2_bytes (128 or 256): what a miss fetches into L2.
 bool make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int64_t ld_bytes,
-                    int box_rows);
+                    int box_rows, int l2_bytes = 256);
 
 // Fused front (front.cu): routing, permutation, quantization and scatter in
 // one cooperative kernel; gs_x null = the global scale is computed from max|x|
