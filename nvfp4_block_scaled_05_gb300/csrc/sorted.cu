@@ -105,9 +105,17 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v) {
   }
 }
 
+// A block deals with one token, or with four, a warp each.
+template <int TOKENS>
+__device__ __forceinline__ void sync_token() {
+  if constexpr (TOKENS > 1) __syncwarp();
+  else __syncthreads();
+}
+
 // The rows of a token's k slots (-1 for a slot without one) and its weights.
 // A row outside [0, n_rows) is an error of the caller's: recorded, and taken
 // as no row. A negative entry is a dropped slot.
+template <int TOKENS>
 __device__ __forceinline__ void load_slots(const Args& a, int64_t t, int64_t* row, float* wt) {
   if ((int)threadIdx.x < a.k) {
     int64_t r = a.f2p[t * a.k + threadIdx.x];
@@ -118,13 +126,51 @@ __device__ __forceinline__ void load_slots(const Args& a, int64_t t, int64_t* ro
     row[threadIdx.x] = r;
     wt[threadIdx.x] = a.w ? a.w[t * a.k + threadIdx.x] : 1.0f;
   }
-  __syncthreads();
+  sync_token<TOKENS>();
 }
 
+// The slots of a block's tokens, in shared memory.
+template <int TOKENS>
+struct Slots {
+  int64_t row[TOKENS][kMaxK];
+  float wt[TOKENS][kMaxK];
+};
+
+// A token's, as its threads read them: kHeld, from registers, else from shared
+// memory as they are needed.
+template <int TOKENS, int KM, bool kHeld>
+struct TokenSlots {
+  const Slots<TOKENS>& s;
+  int k, held_row[KM];
+  float held_wt[KM];
+  __device__ __forceinline__ TokenSlots(const Slots<TOKENS>& slots, int n) : s(slots), k(n) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int j = 0; j < KM; ++j) {
+        held_row[j] = j < k ? (int)s.row[threadIdx.y][j] : -1;
+        held_wt[j] = j < k ? s.wt[threadIdx.y][j] : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ bool has(int j) const {
+    if constexpr (kHeld) return held_row[j] >= 0;
+    else return j < k && s.row[0][j] >= 0;
+  }
+  __device__ __forceinline__ int64_t row(int j) const {
+    if constexpr (kHeld) return held_row[j];
+    else return s.row[0][j];
+  }
+  __device__ __forceinline__ float wt(int j) const {
+    if constexpr (kHeld) return held_wt[j];
+    else return s.wt[0][j];
+  }
+};
+
 // Sums of KM values over the block in a fixed order; thread j < k writes slot j.
-template <int NT, int KM>
+template <int NT, int TOKENS, int KM>
 __device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float (&dot)[KM], const int64_t* row) {
-  __shared__ float part[NT / 32][KM];
+  __shared__ float parts[TOKENS][NT / 32][KM];
+  float(&part)[NT / 32][KM] = parts[TOKENS > 1 ? threadIdx.y : 0];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int j = 0; j < KM; ++j) {
@@ -133,7 +179,7 @@ __device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (lane == 0) part[warp][j] = v;
   }
-  __syncthreads();
+  sync_token<TOKENS>();
   if ((int)threadIdx.x < a.k) {
     float s = 0.0f;
 #pragma unroll
@@ -142,13 +188,23 @@ __device__ __forceinline__ void store_dots(const Args& a, int64_t t, const float
   }
 }
 
+// Slots held in registers help where they leave enough of them: the spread with
+// dots of 16-byte pieces of 16-bit elements for more than four slots (2048 x 4096,
+// k = 8, with the sum before it 80.5 us against 84.5, 256 x 7168 13.8 against 16.8).
+// The sums and pairs of elements lose by it (8192 x 401 63 us against 41), f32 and
+// four slots gain nothing.
+template <int V, int KM, int TOKENS, bool kSpread, bool kDot>
+constexpr bool kHeld = TOKENS > 1 || (V == 8 && KM > 4 && kSpread && kDot);
+
 // One token's row to its k rows. KM >= k slots are unrolled.
-template <typename T, int V, int KM, int NT, bool kDot>
-__global__ void __launch_bounds__(NT) spread_kernel(const Args a) {
-  __shared__ int64_t row[kMaxK];
-  __shared__ float wt[kMaxK];
-  const int64_t t = blockIdx.x;
-  load_slots(a, t, row, wt);
+template <typename T, int V, int KM, int NT, int TOKENS, bool kDot>
+__global__ void __launch_bounds__(NT * TOKENS) spread_kernel(const Args a) {
+  __shared__ Slots<TOKENS> slots;
+  const int local = TOKENS > 1 ? threadIdx.y : 0;
+  const int64_t t = (int64_t)blockIdx.x * TOKENS + local;
+  if (TOKENS > 1 && t >= a.T) return;
+  load_slots<TOKENS>(a, t, slots.row[local], slots.wt[local]);
+  const TokenSlots<TOKENS, KM, kHeld<V, KM, TOKENS, true, kDot>> slot(slots, a.k);
   const T* src = static_cast<const T*>(a.token_in) + t * a.ldt_in;
   float dot[KM];
 #pragma unroll
@@ -163,22 +219,22 @@ __global__ void __launch_bounds__(NT) spread_kernel(const Args a) {
     if constexpr (kDot) {
 #pragma unroll
       for (int j = 0; j < KM; ++j)
-        if (j < a.k && row[j] >= 0)
-          o[j].load(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
+        if (slot.has(j))
+          o[j].load(static_cast<const T*>(a.rows_in) + slot.row(j) * a.ldr_in + c);
     }
     const P x = xr.get(src + c);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      if (j < a.k && row[j] >= 0) {
+      if (slot.has(j)) {
         P y, d;
-        if constexpr (kDot) d = o[j].get(static_cast<const T*>(a.rows_in) + row[j] * a.ldr_in + c);
+        if constexpr (kDot) d = o[j].get(static_cast<const T*>(a.rows_in) + slot.row(j) * a.ldr_in + c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float v = Elem<T>::get(x.e[i]);
-          y.e[i] = Elem<T>::put(wt[j] * v);
+          y.e[i] = Elem<T>::put(slot.wt(j) * v);
           if constexpr (kDot) dot[j] = fmaf(v, Elem<T>::get(d.e[i]), dot[j]);
         }
-        store_pack<T, V>(static_cast<T*>(a.rows_out) + row[j] * a.ldr_out + c, y);
+        store_pack<T, V>(static_cast<T*>(a.rows_out) + slot.row(j) * a.ldr_out + c, y);
       }
     }
   }
@@ -187,23 +243,25 @@ __global__ void __launch_bounds__(NT) spread_kernel(const Args a) {
     const float v = Elem<T>::get(src[c]);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      if (j < a.k && row[j] >= 0) {
-        static_cast<T*>(a.rows_out)[row[j] * a.ldr_out + c] = Elem<T>::put(wt[j] * v);
+      if (slot.has(j)) {
+        static_cast<T*>(a.rows_out)[slot.row(j) * a.ldr_out + c] = Elem<T>::put(slot.wt(j) * v);
         if constexpr (kDot)
-          dot[j] = fmaf(v, Elem<T>::get(static_cast<const T*>(a.rows_in)[row[j] * a.ldr_in + c]), dot[j]);
+          dot[j] = fmaf(v, Elem<T>::get(static_cast<const T*>(a.rows_in)[slot.row(j) * a.ldr_in + c]), dot[j]);
       }
     }
   }
-  if constexpr (kDot) store_dots<NT, KM>(a, t, dot, row);
+  if constexpr (kDot) store_dots<NT, TOKENS, KM>(a, t, dot, slots.row[local]);
 }
 
 // The weighted sum of a token's k rows, in j order, rounded once.
-template <typename T, int V, int KM, int NT, bool kDot>
-__global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
-  __shared__ int64_t row[kMaxK];
-  __shared__ float wt[kMaxK];
-  const int64_t t = blockIdx.x;
-  load_slots(a, t, row, wt);
+template <typename T, int V, int KM, int NT, int TOKENS, bool kDot>
+__global__ void __launch_bounds__(NT * TOKENS) collect_kernel(const Args a) {
+  __shared__ Slots<TOKENS> slots;
+  const int local = TOKENS > 1 ? threadIdx.y : 0;
+  const int64_t t = (int64_t)blockIdx.x * TOKENS + local;
+  if (TOKENS > 1 && t >= a.T) return;
+  load_slots<TOKENS>(a, t, slots.row[local], slots.wt[local]);
+  const TokenSlots<TOKENS, KM, kHeld<V, KM, TOKENS, false, kDot>> slot(slots, a.k);
   const T* rows = static_cast<const T*>(a.rows_in);
   const T* tok = kDot ? static_cast<const T*>(a.token_in) + t * a.ldt_in : nullptr;
   T* out = static_cast<T*>(a.token_out) + t * a.ldt_out;
@@ -218,7 +276,7 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
     Raw<T, V> r[KM], xr;
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-      if (j < a.k && row[j] >= 0) r[j].load(rows + row[j] * a.ldr_in + c);
+      if (slot.has(j)) r[j].load(rows + slot.row(j) * a.ldr_in + c);
     P x;
     if constexpr (kDot) {
       xr.load(tok + c);
@@ -229,12 +287,12 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      if (j < a.k && row[j] >= 0) {
-        const P d = r[j].get(rows + row[j] * a.ldr_in + c);
+      if (slot.has(j)) {
+        const P d = r[j].get(rows + slot.row(j) * a.ldr_in + c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float v = Elem<T>::get(d.e[i]);
-          acc[i] = fmaf(wt[j], v, acc[i]);
+          acc[i] = fmaf(slot.wt(j), v, acc[i]);
           if constexpr (kDot) dot[j] = fmaf(Elem<T>::get(x.e[i]), v, dot[j]);
         }
       }
@@ -250,22 +308,22 @@ __global__ void __launch_bounds__(NT) collect_kernel(const Args a) {
     const float x = kDot ? Elem<T>::get(tok[c]) : 0.0f;
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      if (j < a.k && row[j] >= 0) {
-        const float v = Elem<T>::get(rows[row[j] * a.ldr_in + c]);
-        acc = fmaf(wt[j], v, acc);
+      if (slot.has(j)) {
+        const float v = Elem<T>::get(rows[slot.row(j) * a.ldr_in + c]);
+        acc = fmaf(slot.wt(j), v, acc);
         if constexpr (kDot) dot[j] = fmaf(x, v, dot[j]);
       }
     }
     out[c] = Elem<T>::put(acc);
   }
-  if constexpr (kDot) store_dots<NT, KM>(a, t, dot, row);
+  if constexpr (kDot) store_dots<NT, TOKENS, KM>(a, t, dot, slots.row[local]);
 }
 
-template <typename T, int V, int KM, int NT, bool kSpread, bool kDot>
+template <typename T, int V, int KM, int NT, bool kSpread, bool kDot, int TOKENS = 1>
 void launch_nt(const Args& a, int parts, cudaStream_t s) {
-  const dim3 grid((unsigned)a.T, (unsigned)parts);
-  if constexpr (kSpread) spread_kernel<T, V, KM, NT, kDot><<<grid, NT, 0, s>>>(a);
-  else collect_kernel<T, V, KM, NT, kDot><<<grid, NT, 0, s>>>(a);
+  const dim3 grid((unsigned)ceil_div(a.T, TOKENS), (unsigned)parts), block(NT, TOKENS);
+  if constexpr (kSpread) spread_kernel<T, V, KM, NT, TOKENS, kDot><<<grid, block, 0, s>>>(a);
+  else collect_kernel<T, V, KM, NT, TOKENS, kDot><<<grid, block, 0, s>>>(a);
 }
 
 // Blocks of 64 threads for the sums and the dot products (128 for pairs of
@@ -285,6 +343,10 @@ void launch_nt(const Args& a, int parts, cudaStream_t s) {
 // its dot products, its 256 threads (512 for many pairs: 32 x 7167 BF16 9.5 us
 // against 11.2) see them in fewer rounds (128 tokens: 6.1 against 11.9; from four
 // tokens an SM on, 608: 38.6 against 31.9).
+// Many tokens of a round or two of a warp go four to a block, a warp each, since
+// the blocks' starts are what takes the time: 30000 x 64, k = 2, 17.9 us against
+// 34.0, 8192 x 64, k = 8, 11.8 against 12.5; but 384 columns, k = 8, 26.9 against
+// 26.1. Fewer tokens than 16 an SM are started in time one by one.
 template <typename T, int V, int KM>
 void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
   constexpr int NT = V == 2 && sizeof(T) == 2 ? 128 : 64;
@@ -294,7 +356,12 @@ void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
     const int64_t most = ceil_div(packs, threads), want = ceil_div(blocks, a.T);
     return (int)(most < want ? (most > 0 ? most : 1) : want);
   };
-  if (!dot) {
+  if (packs <= (KM <= 4 ? 64 : 32) && a.T >= 16 * sms) {
+    if (spread && dot) launch_nt<T, V, KM, 32, true, true, 4>(a, 1, s);
+    else if (spread) launch_nt<T, V, KM, 32, true, false, 4>(a, 1, s);
+    else if (dot) launch_nt<T, V, KM, 32, false, true, 4>(a, 1, s);
+    else launch_nt<T, V, KM, 32, false, false, 4>(a, 1, s);
+  } else if (!dot) {
     if (packs <= 224) {
       if (spread) launch_nt<T, V, KM, 32, true, false>(a, parts(32, 16 * sms), s);
       else launch_nt<T, V, KM, 32, false, false>(a, parts(32, 16 * sms), s);

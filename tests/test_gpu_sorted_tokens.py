@@ -65,6 +65,10 @@ CASES = [
     (700, 2, 72, 0, 0.0, 8, 0),
     (650, 16, 500, 0, 0.1, 1, 1),
     (700, 3, 1790, 0, 0.0, 2, 0),
+    (2501, 8, 64, 5, 0.1, 0, 0),        # more tokens still, a warp each
+    (2434, 2, 101, 0, 0.1, 1, 1),
+    (3001, 1, 1, 0, 0.5, 0, 0),
+    (2435, 16, 24, 0, 0.0, 8, 8),
 ]
 
 
