@@ -563,11 +563,11 @@ int fp8_quantize_weight(const void* w, int type, int64_t E, int64_t N, int64_t K
  *            belong to expert e (compact rows, moe_permute's offsets). Bounds
  *            are clamped to [0, M] and to ascending order; rows of no group
  *            are not written.
- *   C        (M, N), leading dimension ldc elements. Stores are 32 bytes wide
- *            where C's rows start on 32-byte boundaries, else one element.
+ *   C        (M, N), leading dimension ldc elements, aligned to an element.
  * The gradient with respect to A is the same product with W's codes and
  * scales transposed. Requires K >= 1, 1 <= E <= 1024; lda and ldw multiples of
- * 16, codes 16-byte aligned. Errors: INVALID, UNSUPPORTED, LAUNCH; a wait that
+ * 16 (large products read rows on 128-byte boundaries up to a third faster),
+ * codes 16-byte aligned. Errors: INVALID, UNSUPPORTED, LAUNCH; a wait that
  * runs out on the device is reported by nvfp4moe_last_device_status.
  */
 int fp8_linear(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, const uint8_t* w_codes,

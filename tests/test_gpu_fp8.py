@@ -282,6 +282,25 @@ def test_strides_and_unaligned_outputs():
         assert (c[:, :shift] == 9).all() and (c[:, shift + N:] == 9).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("N", [3, 131, 256, 300])
+def test_rows_of_c_that_start_anywhere(N, dtype):
+    """Enough rows for the form with 128-row tiles: the values of rows at every
+    alignment are those of rows alone, and nothing beside them is written."""
+    M, K = 80000 if N < 128 else 20100, 144
+    a, sa, w, sw = _operands(M, 1, N, K, 5)
+    want = B.fp8_linear(a, sa, w[0], sw[0], out_dtype=dtype)
+    _check(want[:300], a[:300], sa[:300], w[0], sw[0], dtype, "linear")
+    _check(want[-300:], a[-300:], sa[-300:], w[0], sw[0], dtype, "linear")
+    for pad, shift in [(0, 0), (1, 0), (0, 1), (2, 5), (16, 16), (5, 8), (3, 15), (12, 4), (8, 7), (6, 2)]:
+        ld = N + pad + shift
+        c = torch.full((M, ld), 9.0, dtype=dtype, device=DEV)
+        got = B.fp8_linear(a, sa, w[0], sw[0], out=c[:, shift:shift + N])
+        assert torch.equal(got, want), (pad, shift)
+        assert (c[:, :shift] == 9).all() and (c[:, shift + N:] == 9).all(), (pad, shift)
+    assert B.nvfp4moe_last_device_status() == 0
+
+
 def test_bad_values_stay_in_their_row_and_column():
     M, N, K = 70, 300, 256
     a, sa, w, sw = _operands(M, 1, N, K, 4)
