@@ -329,8 +329,8 @@ void launch_nt(const Args& a, int parts, cudaStream_t s) {
 // Blocks of 64 threads for the sums and the dot products (128 for pairs of
 // 16-bit elements, which take more rounds): more blocks in different phases to
 // an SM (loads, stores, reduction). 8192 x 7168 BF16, k = 8: sum 163 us against
-// 187 with 256 threads, spread with dots 322 against 477, sum with dots 184
-// against 215; pairs, 4096 x 7166: spread with dots 242 against 269 with 64. The
+// 187 with 256 threads, spread with dots 322 against 477 (300 since its slots are
+// in registers), sum with dots 184 against 215; pairs, 4096 x 7166: spread with dots 242 against 269 with 64. The
 // plain spread is better with 256 (162 against 176). Short rows leave threads of
 // such blocks idle, so they get a warp (forward and backward of weighted rows, 8192
 // tokens, k = 8, with a warp / 64, or 128 for pairs: 64 columns 18.2 / 26.0 us, 401
