@@ -568,7 +568,8 @@ int fp8_quantize_weight(const void* w, int type, int64_t E, int64_t N, int64_t K
  * scales transposed. Requires K >= 1, 1 <= E <= 1024; lda and ldw multiples of
  * 16 (large products read rows on 128-byte boundaries up to a third faster),
  * codes 16-byte aligned. Errors: INVALID, UNSUPPORTED, LAUNCH; a wait that
- * runs out on the device is reported by nvfp4moe_last_device_status.
+ * runs out on the device is reported by nvfp4moe_last_device_status, and the
+ * tiles of C that were not complete are not written.
  */
 int fp8_linear(const uint8_t* a_codes, const float* a_sf, int64_t M, int64_t lda, const uint8_t* w_codes,
                const float* w_sf, int64_t N, int64_t K, int64_t ldw, void* c, int c_type, int64_t ldc, void* stream);
@@ -616,7 +617,9 @@ void nvfp4moe_set_wait_limit_ns(uint64_t ns);
  * nothing arrives on, so that bounded wait runs out after the wait limit and
  * the kernel takes its abort path; and block 0 of the fused front
  * (moe_forward_static) leaves before its first grid barrier, so the other
- * blocks' bounded barrier waits run out. Host only; affects launches made
+ * blocks' bounded barrier waits run out. With 2, the 8-bit products make
+ * no factors instead, so that the epilogue's waits run out when the copies and
+ * MMAs of a short product are all issued. Host only; affects launches made
  * afterwards. */
 void nvfp4moe_set_test_stall(int on);
 

@@ -251,7 +251,7 @@ def nvfp4moe_set_wait_limit_ns(ns):
 
 
 def nvfp4moe_set_test_stall(on):
-    lib().nvfp4moe_set_test_stall(1 if on else 0)
+    lib().nvfp4moe_set_test_stall(int(on))
 
 
 def moe_forward_workspace_size(T, K, I, E, k):

@@ -944,7 +944,7 @@ extern "C" int nvfp4moe_last_device_status(void* stream) {
 
 extern "C" void nvfp4moe_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns = ns; }
 
-extern "C" void nvfp4moe_set_test_stall(int on) { g_test_stall = on ? 1 : 0; }
+extern "C" void nvfp4moe_set_test_stall(int on) { g_test_stall = on; }
 
 extern "C" int nvfp4moe_num_sms(void) { return num_sms(); }
 
