@@ -435,7 +435,8 @@ int spread(const void* token, int64_t ldt, int type, int64_t T, int64_t K, int k
   NVFP4_TRY(check_sizes(type, T, K, k, n_rows));
   if (T == 0) return NVFP4MOE_OK;
   NVFP4_CHECK(f2p && (!dot_rows || (w && d_w)) && (dot_rows || !d_w), NVFP4MOE_ERR_INVALID);
-  NVFP4_CHECK(K == 0 || n_rows == 0 || (token && rows), NVFP4MOE_ERR_INVALID);
+  // (a token's row is read before its slots, of which all may be dropped)
+  NVFP4_CHECK(K == 0 || (token && (n_rows == 0 || rows)), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(ldt >= K && ldr >= K && (!dot_rows || ldd >= K), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(element_aligned(token, type) && element_aligned(rows, type) && element_aligned(dot_rows, type),
               NVFP4MOE_ERR_INVALID);
