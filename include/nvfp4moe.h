@@ -499,7 +499,8 @@ int moe_forward_static(const void* x, const float* router_logits, int64_t T, int
  * Sums and dot products in f32, in a fixed order, rounded once.
  *   topk_w  (T, k) f32, or NULL: all weights 1.
  *   d_w     (T, k) f32, given together with the other operand of its dot
- *           products (x, rows) and topk_w, or all NULL: not computed.
+ *           products (x, rows; NULL where that has no elements) and topk_w, or
+ *           all NULL: not computed.
  *   A negative flat_to_perm entry is a dropped slot: nothing is written for it
  *   and it adds nothing (d_w 0). An entry >= n_rows is taken the same way and
  *   records NVFP4MOE_ERR_INVALID in the device status word. Rows that no entry

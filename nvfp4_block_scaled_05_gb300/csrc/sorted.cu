@@ -434,7 +434,7 @@ int spread(const void* token, int64_t ldt, int type, int64_t T, int64_t K, int k
            void* stream) {
   NVFP4_TRY(check_sizes(type, T, K, k, n_rows));
   if (T == 0) return NVFP4MOE_OK;
-  NVFP4_CHECK(f2p && (!dot_rows || (w && d_w)) && (dot_rows || !d_w), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(f2p && (d_w ? w && (dot_rows || n_rows == 0 || K == 0) : !dot_rows), NVFP4MOE_ERR_INVALID);
   // (a token's row is read before its slots, of which all may be dropped)
   NVFP4_CHECK(K == 0 || (token && (n_rows == 0 || rows)), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(ldt >= K && ldr >= K && (!dot_rows || ldd >= K), NVFP4MOE_ERR_INVALID);
@@ -454,7 +454,7 @@ int collect(const void* rows, int64_t n_rows, int64_t ldr, int type, int64_t T, 
             float* d_w, void* stream) {
   NVFP4_TRY(check_sizes(type, T, K, k, n_rows));
   if (T == 0) return NVFP4MOE_OK;
-  NVFP4_CHECK(f2p && (!dot_token || (w && d_w)) && (dot_token || !d_w), NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(f2p && (d_w ? w && (dot_token || K == 0) : !dot_token), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(K == 0 || (token && (n_rows == 0 || rows)), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(ldt >= K && ldr >= K && (!dot_token || ldd >= K), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(element_aligned(token, type) && element_aligned(rows, type) && element_aligned(dot_token, type),
