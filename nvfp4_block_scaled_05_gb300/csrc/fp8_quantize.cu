@@ -243,7 +243,7 @@ int quantize_rows(RowArgs& a, int type, void* stream) {
   NVFP4_CHECK(type_ok(type) && a.rows >= 0 && a.K >= 0 && a.K % 16 == 0 && a.rows < (1ll << 31) && a.K < (1ll << 31),
               NVFP4MOE_ERR_UNSUPPORTED);
   if (a.rows == 0 || a.K == 0) return NVFP4MOE_OK;
-  NVFP4_CHECK(a.x && a.codes && a.sf, NVFP4MOE_ERR_INVALID);
+  NVFP4_CHECK(a.x && (a.n_out == 0 || (a.codes && a.sf)), NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(a.ldx >= (kSwiGLU ? 2 : 1) * a.K && a.ldx * type_bytes(type) % 16 == 0 && aligned(a.x, 16) &&
                   aligned(a.codes, 16) && aligned(a.sf, 4),
               NVFP4MOE_ERR_INVALID);

@@ -42,3 +42,11 @@ def test_weights_gradients_of_no_rows_and_of_no_columns(lib):
     assert sort_back(None, 0, dx=None) == LAUNCH and sort_back(P, 10, d=None, n=0) == LAUNCH
     assert sort_back(None, 10) == INVALID and sort_back(None, 10, d=None, n=0) == INVALID
     assert sort_back(None, 0, w=None) == INVALID
+
+
+def test_rows_quantized_to_no_output_rows(lib):
+    def q(codes, sf, out, f2p=P):
+        return lib.fp8_quantize(P, 0, 4, 64, 64, f2p, 1, out, codes, sf, None)
+    assert q(None, None, 0) == LAUNCH
+    assert q(None, P, 4) == INVALID and q(P, None, 4) == INVALID
+    assert q(None, None, 0, f2p=None) == -2                           # fewer output rows than rows

@@ -40,3 +40,14 @@ def test_no_columns(T, k):
                      B.moe_sort_tokens_backward(rows, f2p, k, topk_w=w, x=x)):
         assert got.numel() == 0 and d_w.shape == (T, k) and (d_w == 0).all()
     assert B.nvfp4moe_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_quantized_to_no_output_rows(dtype):
+    x = torch.ones((7, 528), dtype=dtype, device=DEV)
+    f2p = torch.full((14,), -1, dtype=torch.int32, device=DEV)
+    codes, sf = B.fp8_quantize(x, flat_to_perm=f2p, k=2, out_rows=0)
+    assert codes.shape == (0, 528) and sf.shape == (0, 5) and B.nvfp4moe_last_device_status() == 0
+    f2p[5] = 0
+    B.fp8_quantize(x, flat_to_perm=f2p, k=2, out_rows=0)
+    assert B.nvfp4moe_last_device_status() == -1
