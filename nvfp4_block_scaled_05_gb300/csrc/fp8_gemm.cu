@@ -59,7 +59,8 @@ constexpr int kPartBytes = BN * 4 + 16;  // a row of partial sums in shared memo
 constexpr int kMaxSplit = 8;
 constexpr int kMaxGroups = 1024;
 static_assert(BM * kPartBytes <= OFF_BAR, "the partial sums lie in the ring");
-static_assert(OFF_SCHED + 4 * (3 * kMaxGroups + 1) + 1024 <= 232448, "shared memory budget");
+constexpr int kMaxShared = 232448;       // of a CTA
+static_assert(OFF_SCHED + 4 * (3 * kMaxGroups + 1) + 1024 <= kMaxShared, "shared memory budget");
 
 struct Params {
   const float* a_sf;          // (M, KB)
@@ -1083,11 +1084,34 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   }
 }
 
+constexpr int kMaxDevices = 64;
+
+// Lets a kernel take the shared memory of kMaxGroups groups, once per device
+// (index: one per kernel). The limit is the function's, not a launch's: set to
+// what each call needs, another thread's call could lower it before the launch.
+template <typename Kernel>
+bool allow_shared(Kernel kernel, int index, size_t most) {
+  static std::atomic<bool> known[kMaxDevices][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::atomic<bool>& set = known[dev][index];
+  if (set.load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  set.store(true, std::memory_order_release);
+  return true;
+}
+
+// Dynamic shared memory of a kernel whose schedule of E groups starts at
+// `sched`; the first 1024-byte boundary in it is offset 0.
+constexpr size_t shared_bytes(int sched, int E) { return (size_t)sched + 4 * (3 * (size_t)E + 1) + 1024; }
+
 // Clusters of `split` CTAs of a kernel that fit the device at once, asked once
 // per device (index: one per kernel).
 template <typename Kernel>
 int resident_clusters(Kernel kernel, int index, int threads, size_t smem, int split) {
-  constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices][4][3];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
@@ -1169,13 +1193,6 @@ int64_t tiles_of(const Params& p, int tm) {
   return p.M / tm + (p.E < p.M ? p.E : p.M);
 }
 
-template <typename Kernel>
-bool allow_shared(Kernel kernel, size_t smem) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
-}
-
 template <int NT>
 struct FewLaunch {
   size_t smem;
@@ -1183,9 +1200,10 @@ struct FewLaunch {
   Plan plan;
   bool ok;
   FewLaunch(const Params& p, int sms) {
-    smem = (size_t)Few<NT>::OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
+    smem = shared_bytes(Few<NT>::OFF_SCHED, p.E);
     units = tiles_of(p, NT) * p.NB;
-    ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, smem);
+    ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, NT == 16 ? 6 : NT == 32 ? 7 : 8,
+                                                         shared_bytes(Few<NT>::OFF_SCHED, kMaxGroups));
     if (!ok) return;
     // a block: split 1 of 56 blocks takes 16.4, 18.8 and 29.1 us
     const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, {0.013f, 0.022f, 0.037f}, 4.0f};
@@ -1215,8 +1233,9 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
                     ? (p.c_32B ? fp8_gemm_kernel<__nv_bfloat16, true> : fp8_gemm_kernel<__nv_bfloat16, false>)
                 : p.c_type == NVFP4MOE_F16 ? (p.c_32B ? fp8_gemm_kernel<__half, true> : fp8_gemm_kernel<__half, false>)
                                            : (p.c_32B ? fp8_gemm_kernel<float, true> : fp8_gemm_kernel<float, false>);
-  const size_t smem = (size_t)OFF_SCHED + 4 * (3 * (size_t)p.E + 1) + 1024;
-  if (!allow_shared(kernel, smem)) return NVFP4MOE_ERR_LAUNCH;
+  const size_t smem = shared_bytes(OFF_SCHED, p.E);
+  const int index = 2 * (p.c_type == NVFP4MOE_BF16 ? 0 : p.c_type == NVFP4MOE_F16 ? 1 : 2) + (p.c_32B ? 1 : 0);
+  if (!allow_shared(kernel, index, shared_bytes(OFF_SCHED, kMaxGroups))) return NVFP4MOE_ERR_LAUNCH;
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
