@@ -1109,9 +1109,12 @@ bool allow_shared(Kernel kernel, int index, size_t most) {
 constexpr size_t shared_bytes(int sched, int E) { return (size_t)sched + 4 * (3 * (size_t)E + 1) + 1024; }
 
 // Clusters of `split` CTAs of a kernel that fit the device at once, asked once
-// per device (index: one per kernel).
+// per device (index: one per kernel), with the shared memory of kMaxGroups
+// groups: the answer, and with it the order of a product's sums, is the same
+// whatever was called before. (It counts one CTA to an SM for every kernel
+// that allocates tensor memory, also where two do run on one.)
 template <typename Kernel>
-int resident_clusters(Kernel kernel, int index, int threads, size_t smem, int split) {
+int resident_clusters(Kernel kernel, int index, int threads, size_t most, int split) {
   static std::atomic<int> known[kMaxDevices][4][3];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
@@ -1126,7 +1129,7 @@ int resident_clusters(Kernel kernel, int index, int threads, size_t smem, int sp
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)split, 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = most;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
@@ -1202,13 +1205,13 @@ struct FewLaunch {
   FewLaunch(const Params& p, int sms) {
     smem = shared_bytes(Few<NT>::OFF_SCHED, p.E);
     units = tiles_of(p, NT) * p.NB;
-    ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, NT == 16 ? 6 : NT == 32 ? 7 : 8,
-                                                         shared_bytes(Few<NT>::OFF_SCHED, kMaxGroups));
+    const size_t most = shared_bytes(Few<NT>::OFF_SCHED, kMaxGroups);
+    ok = units * kMaxSplit < (1ll << 31) && allow_shared(fp8_gemm_few_kernel<NT>, NT == 16 ? 6 : NT == 32 ? 7 : 8, most);
     if (!ok) return;
     // a block: split 1 of 56 blocks takes 16.4, 18.8 and 29.1 us
     const Costs costs{NT == 16 ? 0.22f : NT == 32 ? 0.26f : 0.5f, {0.013f, 0.022f, 0.037f}, 4.0f};
     plan = nvfp4moe::plan(units, p.KB, p.M < NT ? p.M : NT, costs, sms, [&](int split) {
-      return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3, kFewThreads, smem, split);
+      return resident_clusters(fp8_gemm_few_kernel<NT>, NT == 16 ? 1 : NT == 32 ? 2 : 3, kFewThreads, most, split);
     });
   }
   int run(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t ldw, Params& p, void* stream) const {
@@ -1235,13 +1238,14 @@ int launch(const uint8_t* a_codes, int64_t lda, const uint8_t* w_codes, int64_t 
                                            : (p.c_32B ? fp8_gemm_kernel<float, true> : fp8_gemm_kernel<float, false>);
   const size_t smem = shared_bytes(OFF_SCHED, p.E);
   const int index = 2 * (p.c_type == NVFP4MOE_BF16 ? 0 : p.c_type == NVFP4MOE_F16 ? 1 : 2) + (p.c_32B ? 1 : 0);
-  if (!allow_shared(kernel, index, shared_bytes(OFF_SCHED, kMaxGroups))) return NVFP4MOE_ERR_LAUNCH;
+  const size_t most = shared_bytes(OFF_SCHED, kMaxGroups);
+  if (!allow_shared(kernel, index, most)) return NVFP4MOE_ERR_LAUNCH;
   const int64_t units = tiles_of(p, BM) * ceil_div(p.N, BN);
   // (groups: the number of tiles is only known on the device; this kernel's
   // CTAs then take them in turn)
   const Costs costs{0.39f, {0.026f, 0.038f, 0.043f}, 6.0f};
   Plan tiles = plan(units, p.KB, p.M < BM ? p.M : BM, costs, sms, [&](int split) {
-    return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, smem, split);
+    return p.offsets ? 0 : resident_clusters(kernel, 0, kThreads, most, split);
   });
   // Few rows: the other kernel where it is estimated to be faster (64 x 4096 x
   // 7168 13.2 us against 16.9, 64 x 16384 x 7168 32.7 against 24.2). Rows of a

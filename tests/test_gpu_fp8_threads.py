@@ -1,9 +1,12 @@
 """8-bit products from several host threads and after calls of other sizes."""
+import subprocess
+import sys
 import threading
 
 import pytest
 import torch
 
+from conftest import ROOT
 from nvfp4_block_scaled_05_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +53,36 @@ def test_threads_with_different_numbers_of_groups():
     torch.cuda.synchronize()
     assert not failed, failed
     assert B.nvfp4moe_last_device_status() == 0
+
+
+ORDER = """
+import sys
+import torch
+sys.path.insert(0, %r)
+from nvfp4_block_scaled_05_gb300 import binding as B
+def product(M, E, N, K):
+    g = torch.Generator().manual_seed(M)
+    a, sa = B.fp8_quantize(torch.randn(M, K, generator=g).cuda())
+    w, sw = B.fp8_quantize_weight(torch.randn(1, N, K, generator=g).cuda())
+    if E == 1:
+        return B.fp8_linear(a, sa, w[0], sw[0], out_dtype=torch.float32)
+    off = torch.linspace(0, M, E + 1).int().cuda()
+    return B.fp8_grouped_gemm(a, sa, w.repeat(E, 1, 1), sw.repeat(E, 1, 1), off, out_dtype=torch.float32)
+shapes = [(1, 1, 4096, 7168), (12, 256, 1024, 7168), (12, 1024, 1024, 7168), (30, 1, 2048, 4096), (20, 1, 4096, 4096)]
+if sys.argv[1] == "1":
+    shapes.reverse()
+out = {s: product(*s).cpu() for s in shapes}
+assert B.nvfp4moe_last_device_status() == 0
+torch.save(out, sys.argv[2])
+"""
+
+
+def test_the_bits_of_a_product_do_not_depend_on_the_calls_before_it(tmp_path):
+    """In a process of its own each, products of many and of few groups in either order."""
+    got = []
+    for order in "01":
+        path = str(tmp_path / order)
+        subprocess.run([sys.executable, "-c", ORDER % ROOT, order, path], check=True, timeout=300)
+        got.append(torch.load(path))
+    for shape, a in got[0].items():
+        assert torch.equal(a, got[1][shape]), shape
