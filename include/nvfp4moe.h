@@ -562,8 +562,8 @@ int fp8_quantize_weight(const void* w, int type, int64_t E, int64_t N, int64_t K
  *            e*N); w_sf (E, ceil(N/128), ceil(K/128)). fp8_linear: E = 1.
  *   offsets  (E + 1) int32 (device): rows [offsets[e], offsets[e+1]) of A and C
  *            belong to expert e (compact rows, moe_permute's offsets). Bounds
- *            are clamped to [0, M] and to ascending order; rows of no group
- *            are not written.
+ *            are clamped to [0, M], and one below an earlier bound counts as
+ *            that one; rows of no group are not written.
  *   C        (M, N), leading dimension ldc elements, aligned to an element.
  * The gradient with respect to A is the same product with W's codes and
  * scales transposed. Requires K >= 1, 1 <= E <= 1024; lda and ldw multiples of

@@ -104,28 +104,37 @@ struct Sched {
   }
 };
 
-// The rows of every group, by all threads. Bounds outside [0, M] or out of
-// order are clamped, so that no tile reaches past the operands whatever the
-// offsets hold.
+// The groups' bounds, by all threads, clamped to [0, M] but not yet in order.
 __device__ __forceinline__ void load_groups(const Params& p, int32_t* start) {
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    int lo = 0, hi = p.M;
-    if (p.offsets) {
-      lo = min(max(p.offsets[e], 0), p.M);
-      hi = min(max(p.offsets[e + 1], lo), p.M);
-    }
-    start[2 * e] = lo;
-    start[2 * e + 1] = hi - lo;
+    start[2 * e] = p.offsets ? min(max(p.offsets[e], 0), p.M) : 0;
+    start[2 * e + 1] = p.offsets ? min(max(p.offsets[e + 1], 0), p.M) : p.M;
   }
 }
 
-// The prefix sum of the groups' tiles, by one warp.
-__device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* tile_start) {
+// The groups' first rows and rows, and the prefix sum of their tiles, by one
+// warp. A group starts at the largest bound so far (a bound below it ends a
+// group where it starts), so that whatever the offsets hold the groups have no
+// row in common, there are no more tiles than the host reckons with, and no
+// tile reaches past the operands.
+__device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* start, int32_t* tile_start) {
   const int lane = threadIdx.x & 31;
-  int carry = 0;
+  int carry = 0, top = 0;
   for (int base = 0; base < sch.E; base += 32) {
     const int e = base + lane;
-    const int mt = e < sch.E ? (sch.start[2 * e + 1] + sch.tm - 1) / sch.tm : 0;
+    int lo = e < sch.E ? start[2 * e] : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, lo, d);
+      if (lane >= d) lo = max(lo, y);
+    }
+    lo = max(lo, top);
+    const int rows = e < sch.E ? max(start[2 * e + 1] - lo, 0) : 0;
+    if (e < sch.E) {
+      start[2 * e] = lo;
+      start[2 * e + 1] = rows;
+    }
+    const int mt = (rows + sch.tm - 1) / sch.tm;
     int incl = mt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -134,6 +143,7 @@ __device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* tile_start
     }
     if (e < sch.E) tile_start[e] = (carry + incl - mt) * sch.NT;
     carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    top = __shfl_sync(0xFFFFFFFFu, lo, 31);
   }
   if (lane == 0) tile_start[sch.E] = carry * sch.NT;
 }
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const Sched sch{start, tile_start, E, NT, p.N, BM, BN};
-  if (warp == 0) scan_tiles(sch, tile_start);
+  if (warp == 0) scan_tiles(sch, start, tile_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -914,7 +924,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (p.offsets) {
-    if (warp == 0) scan_tiles(sch, tile_start);
+    if (warp == 0) scan_tiles(sch, start, tile_start);
     __syncthreads();
     if (unit < tile_start[p.E]) {   // the same for every CTA of a cluster
       sch.decode(unit, e, nb, row0, rows, ncols);
