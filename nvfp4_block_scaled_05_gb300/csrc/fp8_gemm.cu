@@ -60,7 +60,12 @@ constexpr int kMaxSplit = 8;
 constexpr int kMaxGroups = 1024;
 static_assert(BM * kPartBytes <= OFF_BAR, "the partial sums lie in the ring");
 constexpr int kMaxShared = 232448;       // of a CTA
-static_assert(OFF_SCHED + 4 * (3 * kMaxGroups + 1) + 1024 <= kMaxShared, "shared memory budget");
+constexpr int kSharedOfSM = 228 * 1024;  // each CTA on it takes 1 KB more than it asks for
+
+// Dynamic shared memory of a kernel whose schedule of E groups starts at
+// `sched`; the first 1024-byte boundary in it is offset 0.
+constexpr size_t shared_bytes(int sched, int E) { return (size_t)sched + 4 * (2 * (size_t)E + 2) + 1024; }
+static_assert(shared_bytes(OFF_SCHED, kMaxGroups) <= kMaxShared, "shared memory budget");
 
 struct Params {
   const float* a_sf;          // (M, KB)
@@ -83,7 +88,7 @@ struct Params {
 // Tiles of tm activation rows of one group x tn weight rows, ordered
 // group-major, then weight tile, then activation tile.
 struct Sched {
-  const int32_t* start;       // [2E]: first row and rows of every group
+  const int32_t* bounds;      // [E + 1]: first row of every group
   const int32_t* tile_start;  // [E + 1]: first tile of every group
   int E, NT, N, tm, tn;
   __device__ __forceinline__ void decode(int t, int& e, int& nb, int& row0, int& rows, int& ncols) const {
@@ -98,54 +103,51 @@ struct Sched {
     const int local = t - tile_start[e];
     nb = local / mt;
     const int mb = local - nb * mt;
-    row0 = start[2 * e] + mb * tm;
-    rows = min(tm, start[2 * e + 1] - mb * tm);
+    row0 = bounds[e] + mb * tm;
+    rows = min(tm, bounds[e + 1] - row0);
     ncols = min(tn, N - nb * tn);
   }
 };
 
 // The groups' bounds, by all threads, clamped to [0, M] but not yet in order.
-__device__ __forceinline__ void load_groups(const Params& p, int32_t* start) {
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    start[2 * e] = p.offsets ? min(max(p.offsets[e], 0), p.M) : 0;
-    start[2 * e + 1] = p.offsets ? min(max(p.offsets[e + 1], 0), p.M) : p.M;
-  }
+__device__ __forceinline__ void load_bounds(const Params& p, int32_t* bounds) {
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
+    bounds[e] = p.offsets ? min(max(p.offsets[e], 0), p.M) : e == 0 ? 0 : p.M;
 }
 
-// The groups' first rows and rows, and the prefix sum of their tiles, by one
-// warp. A group starts at the largest bound so far (a bound below it ends a
-// group where it starts), so that whatever the offsets hold the groups have no
-// row in common, there are no more tiles than the host reckons with, and no
-// tile reaches past the operands.
-__device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* start, int32_t* tile_start) {
-  const int lane = threadIdx.x & 31;
-  int carry = 0, top = 0;
-  for (int base = 0; base < sch.E; base += 32) {
-    const int e = base + lane;
-    int lo = e < sch.E ? start[2 * e] : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, lo, d);
-      if (lane >= d) lo = max(lo, y);
-    }
-    lo = max(lo, top);
-    const int rows = e < sch.E ? max(start[2 * e + 1] - lo, 0) : 0;
-    if (e < sch.E) {
-      start[2 * e] = lo;
-      start[2 * e + 1] = rows;
-    }
-    const int mt = (rows + sch.tm - 1) / sch.tm;
-    int incl = mt;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += y;
-    }
-    if (e < sch.E) tile_start[e] = (carry + incl - mt) * sch.NT;
-    carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    top = __shfl_sync(0xFFFFFFFFu, lo, 31);
+// The prefix sum of the groups' tiles, by one warp, a run of neighbouring groups
+// a lane. Bounds that do not ascend become the largest so far: whatever the
+// offsets hold, the groups have no row in common, there are no more tiles than
+// the host reckons with, and no tile reaches past the operands.
+__device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* bounds, int32_t* tile_start) {
+  const int lane = threadIdx.x & 31, run = (sch.E + 31) / 32;
+  const int e0 = min(lane * run, sch.E), e1 = min(e0 + run, sch.E);
+  bool ascending = true;
+  int tiles = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int rows = bounds[e + 1] - bounds[e];
+    ascending = ascending && rows >= 0;
+    tile_start[e] = tiles;
+    tiles += (rows + sch.tm - 1) / sch.tm;
   }
-  if (lane == 0) tile_start[sch.E] = carry * sch.NT;
+  if (__builtin_expect(!__all_sync(0xFFFFFFFFu, ascending), 0)) {
+    if (lane == 0)
+      for (int e = 0; e < sch.E; ++e) bounds[e + 1] = max(bounds[e], bounds[e + 1]);
+    __syncwarp();
+    tiles = 0;
+    for (int e = e0; e < e1; ++e) {
+      tile_start[e] = tiles;
+      tiles += (bounds[e + 1] - bounds[e] + sch.tm - 1) / sch.tm;
+    }
+  }
+  int incl = tiles;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  for (int e = e0; e < e1; ++e) tile_start[e] = (incl - tiles + tile_start[e]) * sch.NT;
+  if (lane == 31) tile_start[sch.E] = incl * sch.NT;
 }
 
 // Instruction descriptor: kind::f8f6f4, A and B E4M3 K-major, f32 accumulate.
@@ -544,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   InFlight* in_flight = reinterpret_cast<InFlight*>(smem + OFF_MISC + 16);
   float* scales = reinterpret_cast<float*>(smem + OFF_SCALE);
-  int32_t* start = reinterpret_cast<int32_t*>(smem + OFF_SCHED);
-  int32_t* tile_start = start + 2 * p.E;
+  int32_t* bounds = reinterpret_cast<int32_t*>(smem + OFF_SCHED);
+  int32_t* tile_start = bounds + p.E + 1;
   const int E = p.E, NT = (p.N + BN - 1) / BN;
 
-  load_groups(p, start);
+  load_bounds(p, bounds);
   if (tid == 32) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
@@ -565,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   __syncthreads();
-  const Sched sch{start, tile_start, E, NT, p.N, BM, BN};
-  if (warp == 0) scan_tiles(sch, start, tile_start);
+  const Sched sch{bounds, tile_start, E, NT, p.N, BM, BN};
+  if (warp == 0) scan_tiles(sch, bounds, tile_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -805,9 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the CTAs: with few rows the product is a stream of the weights from HBM, and
 // what counts is that every SM keeps loads in flight. One unit of work is one
 // tile and one range of its blocks of K (a cluster of `split` CTAs shares a
-// tile); a stage is small enough for two CTAs on an SM, so that one unit's
-// loads run under another's beginning and end. The sums leave through shared
-// memory, since a lane holds a column of C, joined over the cluster.
+// tile); a stage is small enough for two CTAs on an SM (for 16 rows with up to
+// 343 groups), so that one unit's loads run under another's beginning and end
+// (8 rows of 256 groups, 4096 x 7168: 41.2 us; one CTA 47.7). The sums leave
+// through shared memory, since a lane holds a column of C, joined over the
+// cluster.
 // Warp roles (256 threads): 0 producer, 1 MMA, 2 factors, 4-7 epilogue. (Eight
 // epilogue warps for 64 rows measured the same: 14.5 us against 14.3 at
 // 64 x 4096 x 7168.)
@@ -829,6 +833,7 @@ struct Few {
   static constexpr uint32_t TMEM = BUFS * NT;
   static_assert(NT * PART_BYTES <= OFF_BAR, "the partial sums lie in the ring");
   static_assert(BUFS <= STAGES, "a barrier of a stage would complete twice unseen");
+  static_assert(2 * (shared_bytes(OFF_SCHED, 256) + 1024) <= kSharedOfSM, "two CTAs on an SM");
 };
 
 constexpr int kFewThreads = 256;
@@ -855,9 +860,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   InFlight* in_flight = reinterpret_cast<InFlight*>(smem + C::OFF_MISC + 16);
   float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
-  int32_t* start = reinterpret_cast<int32_t*>(smem + C::OFF_SCHED);
-  int32_t* tile_start = start + 2 * p.E;
-  const Sched sch{start, tile_start, p.E, p.NB, p.N, NT, 128};
+  int32_t* bounds = reinterpret_cast<int32_t*>(smem + C::OFF_SCHED);
+  int32_t* tile_start = bounds + p.E + 1;
+  const Sched sch{bounds, tile_start, p.E, p.NB, p.N, NT, 128};
 
   const int split = p.split;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
@@ -875,7 +880,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     ncols = min(128, p.N - nb * 128);
     blocks_of_k();
   } else {
-    load_groups(p, start);
+    load_bounds(p, bounds);
   }
   // the producer's state (thread 0)
   uint32_t p_stage = 0, p_phase = 0, filled = 0, fill_phase = 0;
@@ -924,7 +929,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (p.offsets) {
-    if (warp == 0) scan_tiles(sch, start, tile_start);
+    if (warp == 0) scan_tiles(sch, bounds, tile_start);
     __syncthreads();
     if (unit < tile_start[p.E]) {   // the same for every CTA of a cluster
       sch.decode(unit, e, nb, row0, rows, ncols);
@@ -1113,10 +1118,6 @@ bool allow_shared(Kernel kernel, int index, size_t most) {
   set.store(true, std::memory_order_release);
   return true;
 }
-
-// Dynamic shared memory of a kernel whose schedule of E groups starts at
-// `sched`; the first 1024-byte boundary in it is offset 0.
-constexpr size_t shared_bytes(int sched, int E) { return (size_t)sched + 4 * (3 * (size_t)E + 1) + 1024; }
 
 // Clusters of `split` CTAs of a kernel that fit the device at once, asked once
 // per device (index: one per kernel), with the shared memory of kMaxGroups
