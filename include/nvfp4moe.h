@@ -541,6 +541,8 @@ int moe_unsort_tokens_backward(const void* dy, int type, int64_t T, int64_t K, i
  *   codes (out_rows, K) bytes, 16-byte aligned; sf (out_rows, ceil(K/128)) f32.
  * fp8_swiglu_quantize -- the same of h = silu(gate) * up, silu(g) =
  *   g / (1 + exp(-g)) in f32, for rows [gate 0..I-1 | up 0..I-1] of gate_up.
+ *   h is within 2^-20 (relative) of it for every gate whose exp(-g) is finite
+ *   in f32, and 0 below.
  * fp8_quantize_weight -- w (E, N, K), rows ldw elements apart, into 128 x 128
  *   blocks: codes (E, N, K) bytes, sf (E, ceil(N/128), ceil(K/128)) f32.
  * Sources: base address and row stride multiples of 16 bytes; K (I) a multiple

@@ -14,8 +14,8 @@
 // quantized once and stored k times. Measured: 8192 x 7168 BF16 to 8 experts
 // each 94 us, 6.4 TB/s of 6.76 (a plain copy's); to one place 31.7 us, 5.6
 // TB/s; 8 x 4096 x 7168 BF16 weights 100 us, 7.0 TB/s. The SwiGLU form is near the
-// bound of its arithmetic with 16-bit sources (16384 x 2048 BF16 29.8 us, 5.7
-// TB/s; F32 47.8 us, 6.3 TB/s).
+// bound of its arithmetic with 16-bit sources (16384 x 2048 BF16 30.1 us, 5.6
+// TB/s; F32 48.4 us, 6.2 TB/s).
 #include "common.cuh"
 
 #include <cuda_fp16.h>
@@ -98,16 +98,61 @@ __device__ __forceinline__ float block_scale(float amax, float& inv) {
   return __fdiv_rn(amax, kE4M3Max);
 }
 
-// silu(g) * u = g / (1 + exp(-g)) * u with the exponential and reciprocal
-// instructions, exp(-g) as 2^(-g log2(e)): within 2^-21 + |g| 2^-24 of it (the
-// last from the rounding of the exponent), which is far below half a step of
-// E4M3, 2^-4. Where exp(-g) overflows, the quotient is 0. (The division and
-// expf of CUDA's library: 45 us at 16384 x 2048 BF16; this: 29.8.)
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(-g, 0x1.715476p+0f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
-  return __fmul_rn(__fmul_rn(g, r), u);
+// Two f32 operations in one instruction (a register pair each).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float a) { return pair(a, a); }
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// v = silu(g) * u = g / (1 + exp(-g)) * u for two elements, within 2^-20 of it
+// down to the g whose exp(-g) is an f32, below which it is 0.
+//   exp(-g) = 2^t 2^d, t = -g log2(e) rounded to f32 and d the rest of the
+//   product, which is up to 2^-18 and in which t would be wrong by as much:
+//   2^d = 1 + d ln(2) in f32.
+//   g / (1 + exp(-g)) = g/4 / ((1 + exp(-g)) / 4), since the reciprocal
+//   instruction has no results below 2^-126.
+// Where t overflows d is no number, and is taken as one that changes nothing.
+// (16384 x 2048 BF16: 30.1 us; without d 28.8, and up to 2^-18 off; with the
+// exponential and the division of CUDA's library 45.)
+__device__ __forceinline__ void silu_mul2(float& v0, float& v1, float u0, float u1) {
+  constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
+  constexpr float kHi = (float)kLog2e, kLo = (float)((kLog2e - (double)kHi) * kLn2);
+  const uint64_t g = pair(v0, v1);
+  const uint64_t t = mul2(g, pair(-kHi));
+  const uint64_t rest = fma2(g, pair(kHi), t);                     // -d without the low part of log2(e)
+  const uint64_t k = fma2(g, pair(-kLo), fma2(rest, pair(-(float)kLn2), pair(1.0f)));
+  float t0, t1, k0, k1, d0, d1;
+  unpair(t, t0, t1);
+  unpair(k, k0, k1);
+  const uint64_t e = mul2(pair(ex2(t0), ex2(t1)), pair(fminf(k0, 2.0f), fminf(k1, 2.0f)));
+  unpair(fma2(e, pair(0.25f), pair(0.25f)), d0, d1);
+  const uint64_t s = mul2(mul2(g, pair(0.25f)), pair(rcp(d0), rcp(d1)));
+  unpair(mul2(s, pair(u0, u1)), v0, v1);
 }
 
 // 16 codes, element 0 in the lowest byte.
@@ -170,7 +215,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_rows_fp8_kernel(const
     if (valid) x.load(p + a.K);
     to_f32(x, u);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = silu_mul(v[i], u[i]);
+    for (int i = 0; i < 16; i += 2) silu_mul2(v[i], v[i + 1], u[i], u[i + 1]);
   }
   float m = amax16(v);
 #pragma unroll
