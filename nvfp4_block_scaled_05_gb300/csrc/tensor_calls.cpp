@@ -13,6 +13,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+#include <string>
+
 #include "nvfp4moe.h"
 
 namespace {
@@ -73,10 +76,30 @@ Matrix matrix(PyObject* o, const char* name, bool codes = false) {
   return Matrix{t, n, c, n > 1 ? ld : (ld > c ? ld : c), t.data_ptr(), codes ? -1 : type};
 }
 
-void* flat(PyObject* o, const char* name, at::ScalarType type, int64_t numel) {
+// Whether t, which is contiguous, is a tensor of these sizes, but for sizes of
+// 1, or their elements in one dimension. (The number of elements alone would
+// take a transposed one.)
+bool has_sizes(const at::Tensor& t, std::initializer_list<int64_t> sizes) {
+  int64_t numel = 1;
+  for (const int64_t s : sizes) numel *= s;
+  if (t.dim() == 1 || t.numel() != numel) return t.numel() == numel;
+  int64_t d = 0;
+  for (const int64_t s : sizes) {
+    if (s == 1) continue;
+    while (d < t.dim() && t.size(d) == 1) ++d;
+    if (d == t.dim() || t.size(d++) != s) return false;
+  }
+  while (d < t.dim() && t.size(d) == 1) ++d;
+  return d == t.dim();
+}
+
+void* flat(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> sizes) {
   const at::Tensor& t = on_gpu(o, name);
-  if (!t.is_contiguous() || t.scalar_type() != type || t.numel() != numel)
-    REFUSE("%s must be contiguous and have %lld elements of %s", name, (long long)numel, c10::toString(type));
+  if (!t.is_contiguous() || t.scalar_type() != type || !has_sizes(t, sizes)) {
+    std::string dims;
+    for (const int64_t s : sizes) dims += (dims.empty() ? "" : " x ") + std::to_string(s);
+    REFUSE("%s must be contiguous, %s of %s", name, dims.c_str(), c10::toString(type));
+  }
   return t.data_ptr();
 }
 
@@ -102,10 +125,11 @@ struct Slots {
 Slots slots(PyObject* f2p, PyObject* k, PyObject* w) {
   const at::Tensor& t = on_gpu(f2p, "flat_to_perm");
   const int64_t kk = integer(k, "k"), n = t.numel();
-  if (!t.is_contiguous() || t.scalar_type() != at::kInt || kk < 1 || kk > 16 || n % kk != 0)
+  if (!t.is_contiguous() || t.scalar_type() != at::kInt || kk < 1 || kk > 16 || n % kk != 0 ||
+      !has_sizes(t, {n / kk, kk}))
     REFUSE("flat_to_perm must be contiguous int32 with k entries a token, 1 <= k <= 16");
   return Slots{n / kk, (int)kk, static_cast<const int32_t*>(t.data_ptr()),
-               none(w) ? nullptr : static_cast<const float*>(flat(w, "topk_w", at::kFloat, n))};
+               none(w) ? nullptr : static_cast<const float*>(flat(w, "topk_w", at::kFloat, {n / kk, kk}))};
 }
 
 // The operand of the weights' gradient, and the gradient.
@@ -236,14 +260,14 @@ Quantized quantized(PyObject* codes, PyObject* sf, int64_t n, int64_t K, const a
     q.codes = at::empty({n, K}, like.options().dtype(at::kByte));
     q.pc = static_cast<uint8_t*>(q.codes.data_ptr());
   } else {
-    q.pc = static_cast<uint8_t*>(flat(codes, "codes", at::kByte, n * K));
+    q.pc = static_cast<uint8_t*>(flat(codes, "codes", at::kByte, {n, K}));
     q.codes = THPVariable_Unpack(codes);
   }
   if (none(sf)) {
     q.sf = at::empty({n, blocks(K)}, like.options().dtype(at::kFloat));
     q.ps = static_cast<float*>(q.sf.data_ptr());
   } else {
-    q.ps = static_cast<float*>(flat(sf, "sf", at::kFloat, n * blocks(K)));
+    q.ps = static_cast<float*>(flat(sf, "sf", at::kFloat, {n, blocks(K)}));
     q.sf = THPVariable_Unpack(sf);
   }
   return q;
@@ -309,8 +333,8 @@ CALL(fp8_linear, 6)
   const Matrix x = matrix(a[0], "a_codes", true), w = matrix(a[2], "w_codes", true);
   if (w.c != x.c) REFUSE("a_codes and w_codes must have the same K");
   const int64_t kb = blocks(x.c);
-  const auto* sx = static_cast<const float*>(flat(a[1], "a_sf", at::kFloat, x.n * kb));
-  const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, blocks(w.n) * kb));
+  const auto* sx = static_cast<const float*>(flat(a[1], "a_sf", at::kFloat, {x.n, kb}));
+  const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, {blocks(w.n), kb}));
   const Matrix out = output(a[4], "out", x.n, w.n, x.t, product_type(a[4], a[5]));
   run("fp8_linear", [&](void* st) {
     return ::fp8_linear(static_cast<const uint8_t*>(x.p), sx, x.n, x.ld, static_cast<const uint8_t*>(w.p), sw, w.n,
@@ -327,9 +351,9 @@ CALL(fp8_grouped_gemm, 7)
     REFUSE("w_codes must be contiguous (E, N, K) codes with the K of a_codes");
   const int64_t E = w.size(0), N = w.size(1), kb = blocks(x.c);
   if (E > 1024) REFUSE("at most 1024 experts");
-  const auto* sx = static_cast<const float*>(flat(a[1], "a_sf", at::kFloat, x.n * kb));
-  const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, E * blocks(N) * kb));
-  const auto* off = static_cast<const int32_t*>(flat(a[4], "offsets", at::kInt, E + 1));
+  const auto* sx = static_cast<const float*>(flat(a[1], "a_sf", at::kFloat, {x.n, kb}));
+  const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, {E, blocks(N), kb}));
+  const auto* off = static_cast<const int32_t*>(flat(a[4], "offsets", at::kInt, {E + 1}));
   const Matrix out = output(a[5], "out", x.n, N, x.t, product_type(a[5], a[6]));
   run("fp8_grouped_gemm", [&](void* st) {
     return ::fp8_grouped_gemm(static_cast<const uint8_t*>(x.p), sx, x.n, x.ld,
