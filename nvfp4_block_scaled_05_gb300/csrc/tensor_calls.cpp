@@ -73,7 +73,8 @@ Matrix matrix(PyObject* o, const char* name, bool codes = false) {
   const int64_t n = t.size(0), c = t.size(1), ld = t.stride(0);
   if ((c > 1 && t.stride(1) != 1) || (n > 1 && ld < c))
     REFUSE("the rows of %s must be contiguous and must not overlap", name);
-  return Matrix{t, n, c, n > 1 ? ld : (ld > c ? ld : c), t.data_ptr(), codes ? -1 : type};
+  // no second row keeps to a single one's stride, which any entry point then takes
+  return Matrix{t, n, c, n > 1 ? ld : (c + 15) / 16 * 16, t.data_ptr(), codes ? -1 : type};
 }
 
 // Whether t, which is contiguous, is a tensor of these sizes, but for sizes of

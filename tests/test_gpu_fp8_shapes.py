@@ -60,3 +60,26 @@ def test_slots_and_weights():
     _refused(lambda: B.moe_unsort_tokens(rows, f2p, k, topk_w=w.t().contiguous()))
     _refused(lambda: B.moe_unsort_tokens_backward(x, f2p.view(k, T), k, topk_w=w, rows=rows))
     assert torch.equal(B.moe_sort_tokens(x, f2p.view(T, k), k, topk_w=w.view(-1)), rows)
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    """One row of a wider matrix, whose stride no second row has to keep to."""
+    wide = torch.randn(3, 512 + 5, generator=torch.Generator().manual_seed(7)).to(DEV)
+    x = wide[:1, :512]
+    codes, sf = B.fp8_quantize(x)
+    want = B.fp8_quantize(x.contiguous())
+    assert torch.equal(codes, want[0]) and torch.equal(sf, want[1])
+    for got, want in zip(B.fp8_swiglu_quantize(x), B.fp8_swiglu_quantize(x.contiguous())):
+        assert torch.equal(got, want)
+    _, _, w, sw, _ = _operands()
+    a = torch.zeros((2, 512 + 7), dtype=torch.uint8, device=DEV)[:1, :512]
+    a.copy_(codes)
+    one = B.fp8_linear(codes, sf, w[0], sw[0])
+    assert torch.equal(B.fp8_linear(a, sf, w[0], sw[0]), one)
+    row = torch.zeros((2, 512 + 9), dtype=torch.uint8, device=DEV)[:1, :512]
+    row.copy_(w[0, :1])
+    assert torch.equal(B.fp8_linear(codes, sf, row, sw[0, :1]), B.fp8_linear(codes, sf, w[0, :1], sw[0, :1]))
+    out = torch.zeros((2, 301), dtype=torch.bfloat16, device=DEV)[:1, :300]
+    assert torch.equal(B.fp8_linear(codes, sf, w[0], sw[0], out=out), one)
+    f2p = torch.tensor([1, 0], dtype=torch.int32, device=DEV)
+    assert torch.equal(B.moe_sort_tokens(x, f2p, 2), x.expand(2, 512))
