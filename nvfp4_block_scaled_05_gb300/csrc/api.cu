@@ -312,8 +312,13 @@ Fp8Layout fp8_layout(int64_t T, int64_t K, int64_t I, int E, int k) {
 }
 
 bool fp8_shape_ok(int64_t T, int64_t K, int64_t I, int E, int k) {
-  return T >= 0 && K > 0 && K % 16 == 0 && K < (1ll << 24) && I > 0 && I % 16 == 0 && I < (1ll << 24) && k >= 1 &&
-         k <= 16 && E >= k && E <= 1024 && T * k < (1ll << 31) - 128;
+  if (!(T >= 0 && T < (1ll << 31) && K > 0 && K % 16 == 0 && K < (1ll << 24) && I > 0 && I % 16 == 0 && I < (1ll << 24) &&
+        k >= 1 && k <= 16 && E >= k && E <= 1024 && T * k < (1ll << 31) - 128))
+    return false;
+  // the stages' own: weight rows and tiles of the products, pieces of 512 elements of the quantizers
+  const int64_t M = T * k, widest = 2 * I > K ? 2 * I : K;
+  return E * widest < (1ll << 31) - 256 && (ceil_div(M, 128) + E) * ceil_div(widest, 256) < (1ll << 31) &&
+         T * ceil_div(K, 512) < (1ll << 32) - 8 && M * ceil_div(I, 512) < (1ll << 32) - 8;
 }
 
 }  // namespace
