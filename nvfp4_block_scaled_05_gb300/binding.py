@@ -511,13 +511,16 @@ def fp8_moe_forward(x, logits, weights, k, ws=None, y=None):
     for t, name, dtype, shape in ((logits, "logits", torch.float32, (T, E)), (y, "y", torch.bfloat16, (T, K))):
         if t is not None and (_dev(t, name).dtype != dtype or tuple(t.shape) != shape):
             raise NVFP4Error("%s must be %dx%d of %s" % (name, *shape, dtype))
+    for name in ("w1_codes", "w1_sf", "w2_codes", "w2_sf"):
+        _dev(weights[name], name)
     if ws is None:
         ws = torch.empty(fp8_moe_forward_workspace_size(T, K, I, E, k), dtype=torch.uint8, device=x.device)
+    _dev(ws, "ws")
     if y is None:
         y = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
     _check(lib().fp8_moe_forward(_ptr(x), _ptr(logits), T, K, I, E, k, _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]),
-                                 _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]), _ptr(y), _ptr(ws), ws.numel(),
-                                 _stream()), "fp8_moe_forward")
+                                 _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]), _ptr(y), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream()), "fp8_moe_forward")
     return y
 
 
