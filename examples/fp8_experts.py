@@ -19,37 +19,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from nvfp4_block_scaled_05_gb300 import binding as B  # noqa: E402
 
 
-class SortTokens(torch.autograd.Function):
-    """x (T, K) -> the rows of every expert in turn."""
-
-    @staticmethod
-    def forward(ctx, x, flat_to_perm, k):
-        ctx.save_for_backward(flat_to_perm)
-        ctx.k = k
-        return B.moe_sort_tokens(x, flat_to_perm, k)
-
-    @staticmethod
-    def backward(ctx, d_rows):
-        (flat_to_perm,) = ctx.saved_tensors
-        return B.moe_sort_tokens_backward(d_rows.contiguous(), flat_to_perm, ctx.k)[0], None, None
-
-
-class UnsortTokens(torch.autograd.Function):
-    """The experts' rows -> the weighted sum over each token's experts."""
-
-    @staticmethod
-    def forward(ctx, rows, topk_w, flat_to_perm, k):
-        ctx.save_for_backward(rows, topk_w, flat_to_perm)
-        ctx.k = k
-        return B.moe_unsort_tokens(rows, flat_to_perm, k, topk_w=topk_w)
-
-    @staticmethod
-    def backward(ctx, dy):
-        rows, topk_w, flat_to_perm = ctx.saved_tensors
-        d_rows, d_w = B.moe_unsort_tokens_backward(dy.contiguous(), flat_to_perm, ctx.k, topk_w=topk_w, rows=rows)
-        return d_rows, d_w, None, None
-
-
 def experts(rows, offsets, w1, w2):
     """silu(gate) * up and the down projection, expert by expert."""
     bounds = offsets.tolist()
@@ -83,7 +52,8 @@ def main():
     xg, wg = x.clone().requires_grad_(), w.clone().requires_grad_()
     w1g, w2g = w1.clone().requires_grad_(), w2.clone().requires_grad_()
     target = torch.randn(T, K, device=dev, generator=g).bfloat16()
-    y = UnsortTokens.apply(experts(SortTokens.apply(xg, flat_to_perm, k), offsets, w1g, w2g), wg, flat_to_perm, k)
+    rows = experts(B.moe_sort_tokens(xg, flat_to_perm, k), offsets, w1g, w2g)
+    y = B.moe_unsort_tokens(rows, flat_to_perm, k, topk_w=wg)
     loss = (y.float() - target.float()).square().mean()
     loss.backward()
     xr, wr = x.float().requires_grad_(), w.clone().requires_grad_()

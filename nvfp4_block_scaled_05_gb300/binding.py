@@ -428,27 +428,73 @@ def moe_combine(out, topk_w, flat_to_perm, y=None):
 
 # ------------------------------------------------------------------ tokens in expert order
 
+def _given(ctx, out, name):
+    """The caller's output, which the backward pass takes for a new tensor."""
+    if out is not None:
+        if out.requires_grad:
+            raise NVFP4Error("%s must not require gradients of its own" % name)
+        ctx.mark_dirty(out)
+
+
+class _SortTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, topk_w, flat_to_perm, k, n_rows, rows):
+        _given(ctx, rows, "rows")
+        ctx.k, weighted = k, ctx.needs_input_grad[1]
+        ctx.save_for_backward(x if weighted else None, topk_w, flat_to_perm)
+        return _calls().moe_sort_tokens(x, flat_to_perm, k, topk_w, n_rows, rows)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_rows):
+        x, topk_w, flat_to_perm = ctx.saved_tensors
+        dx, d_w = moe_sort_tokens_backward(d_rows.contiguous(), flat_to_perm, ctx.k, topk_w, x)
+        return dx, None if d_w is None else d_w.view_as(topk_w), None, None, None, None
+
+
+class _UnsortTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, topk_w, flat_to_perm, k, y):
+        _given(ctx, y, "y")
+        ctx.k, weighted, ctx.shape = k, ctx.needs_input_grad[1], rows.shape
+        ctx.save_for_backward(rows if weighted else None, topk_w, flat_to_perm)
+        return _calls().moe_unsort_tokens(rows, flat_to_perm, k, topk_w, y)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        rows, topk_w, flat_to_perm = ctx.saved_tensors
+        dy = dy.contiguous()
+        # rows that no entry names have a gradient of zero, and which they are the device knows
+        d_rows, d_w = moe_unsort_tokens_backward(dy, flat_to_perm, ctx.k, topk_w, rows, d_rows=dy.new_zeros(ctx.shape))
+        return d_rows, None if d_w is None else d_w.view_as(topk_w), None, None, None
+
+
 def moe_sort_tokens(x, flat_to_perm, k, topk_w=None, n_rows=None, rows=None):
     """x (T, K) in expert order: rows[flat_to_perm[t*k+j]] = topk_w[t, j] * x[t]
-    (n_rows rows, T*k if not given; those that no entry names are not written)."""
-    return _calls().moe_sort_tokens(x, flat_to_perm, k, topk_w, n_rows, rows)
+    (n_rows rows, T*k if not given; those that no entry names are not written).
+    Differentiable in x and topk_w, once."""
+    out = _calls().moe_sort_tokens(x, flat_to_perm, k, topk_w, n_rows, rows)
+    return _SortTokens.apply(x, topk_w, flat_to_perm, k, n_rows, rows) if out is NotImplemented else out
 
 
 def moe_sort_tokens_backward(d_rows, flat_to_perm, k, topk_w=None, x=None, dx=None):
-    """The gradients of moe_sort_tokens: (dx, d_w); d_w is computed when x (and
-    topk_w) is given, else None."""
+    """The gradients of moe_sort_tokens: (dx, d_w); d_w is computed when x is
+    given (together with topk_w), else None. Not differentiable."""
     return _calls().moe_sort_tokens_backward(d_rows, flat_to_perm, k, topk_w, x, dx)
 
 
 def moe_unsort_tokens(rows, flat_to_perm, k, topk_w=None, y=None):
-    """y[t] = sum_j topk_w[t, j] * rows[flat_to_perm[t*k+j]]."""
-    return _calls().moe_unsort_tokens(rows, flat_to_perm, k, topk_w, y)
+    """y[t] = sum_j topk_w[t, j] * rows[flat_to_perm[t*k+j]]. Differentiable in
+    rows and topk_w, once."""
+    out = _calls().moe_unsort_tokens(rows, flat_to_perm, k, topk_w, y)
+    return _UnsortTokens.apply(rows, topk_w, flat_to_perm, k, y) if out is NotImplemented else out
 
 
 def moe_unsort_tokens_backward(dy, flat_to_perm, k, topk_w=None, rows=None, n_rows=None, d_rows=None):
     """The gradients of moe_unsort_tokens: (d_rows, d_w); d_w is computed when
-    rows (and topk_w) is given, else None. Rows that no entry of flat_to_perm
-    names are not written."""
+    rows is given (together with topk_w), else None. Rows that no entry of
+    flat_to_perm names are not written. Not differentiable."""
     return _calls().moe_unsort_tokens_backward(dy, flat_to_perm, k, topk_w, rows, n_rows, d_rows)
 
 

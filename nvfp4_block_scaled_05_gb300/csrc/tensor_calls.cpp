@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -191,8 +192,16 @@ int64_t blocks(int64_t n) { return (n + 127) / 128; }
   END_HANDLE_TH_ERRORS    \
   }
 
+// Whether a call on this tensor has to be recorded for a backward pass:
+// binding.py then makes it again through an autograd function (in which
+// gradients are not recorded).
+bool recorded(PyObject* o) {
+  return !none(o) && c10::GradMode::is_enabled() && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad();
+}
+
 // x, flat_to_perm, k, topk_w, n_rows, rows
 CALL(moe_sort_tokens, 6)
+  if (recorded(a[0]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Matrix x = matrix(a[0], "x");
   const Slots s = slots(a[1], a[2], a[3]);
   if (s.tokens != x.n) REFUSE("flat_to_perm must have k entries for each row of x");
@@ -220,6 +229,7 @@ END_CALL
 
 // rows, flat_to_perm, k, topk_w, y
 CALL(moe_unsort_tokens, 5)
+  if (recorded(a[0]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Matrix r = matrix(a[0], "rows");
   const Slots s = slots(a[1], a[2], a[3]);
   const Matrix out = output(a[4], "y", s.tokens, r.c, r.t, r.t.scalar_type());
