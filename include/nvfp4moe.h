@@ -620,9 +620,10 @@ void nvfp4moe_set_wait_limit_ns(uint64_t ns);
  * nothing arrives on, so that bounded wait runs out after the wait limit and
  * the kernel takes its abort path; and block 0 of the fused front
  * (moe_forward_static) leaves before its first grid barrier, so the other
- * blocks' bounded barrier waits run out. With 2, the 8-bit products make
- * no factors instead, so that the epilogue's waits run out when the copies and
- * MMAs of a short product are all issued. Host only; affects launches made
+ * blocks' bounded barrier waits run out. With 2, the epilogue of the NVFP4
+ * products stalls instead, and the 8-bit products make no factors, so that
+ * their epilogue's waits run out: the copies and MMAs of a short product are
+ * then all issued. Host only; affects launches made
  * afterwards. */
 void nvfp4moe_set_test_stall(int on);
 

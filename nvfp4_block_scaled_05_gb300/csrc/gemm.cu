@@ -53,9 +53,10 @@
 // barriers.
 //
 // Every wait is bounded: a wait that exceeds the limit sets the device status
-// word, raises a shared abort flag that ends the other roles' loops, and the
-// CTA then waits (with a fixed bound) for its own copies and tensor-core work
-// in flight, frees its tensor memory and returns.
+// word and raises a shared abort flag that ends the other roles' loops. Once
+// all roles have ended, the CTA waits (with a fixed bound) for its own copies
+// and tensor-core work in flight, whichever role gave up, frees its tensor
+// memory and returns.
 #include "common.cuh"
 
 #include <atomic>
@@ -130,7 +131,7 @@ struct Params {
   const float* gs_h;
   uint64_t wait_limit_ns;
   int* status;
-  int test_stall;             // test hook: the MMA issuer first waits on a barrier nobody arrives on
+  int test_stall;             // test hook: 1: the MMA issuer, 2: the epilogue first waits on a barrier nobody arrives on
 };
 
 // Work units, ordered expert-major, then weight tile, then activation tile(s).
@@ -199,6 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_exit = bar_sffull + STAGES * 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  // what the roles have in flight when they end, for the drain after an abort:
+  // it may come from a role that waits on the others' work, while they have
+  // issued all of theirs and ended as usual
+  uint32_t* in_flight = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 16);
   int32_t* tile_start = reinterpret_cast<int32_t*>(smem + C::OFF_SCHED);
   int32_t* pad_off = tile_start + (p.E + 1);
   const int E = p.E, NT = (p.N + BN - 1) / BN;
@@ -364,30 +369,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       cur = nxt;
     }
-    if (!ok) {
-      // copies still in flight complete before the CTA may exit. A pair's
-      // copies complete on the even CTA's barriers together with the other
-      // CTA's, whose producer may have stopped before arming or issuing its
-      // part, so a pair waits a fixed time instead: far longer than a copy
-      // takes to land (microseconds), and both CTAs then still pass the exit
-      // handshake, so neither leaves while the other's copies may land.
-      if constexpr (kPair) {
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < kPairCopyDrainNs) {
-        }
-      } else {
-        for (int s = 0; s < STAGES; ++s)
-          if ((filled >> s) & 1u) drain_wait(bar_full + 8 * s, (fill_phase >> s) & 1u);
-      }
-    } else if constexpr (kPair) {
-      // every stage's last use released by the even CTA's MMAs (whose commits
-      // arrive on this CTA's barriers) before the CTA may exit
-      for (int i = 0; i < STAGES; ++i) {
-        if (!wait_bounded(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 10, peer_abort))
-          break;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
+    in_flight[0] = filled;
+    in_flight[1] = fill_phase;
+    if constexpr (kPair) {
+      if (ok) {
+        // every stage's last use released by the even CTA's MMAs (whose commits
+        // arrive on this CTA's barriers) before the CTA may exit
+        for (int i = 0; i < STAGES; ++i) {
+          if (!wait_bounded(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.wait_limit_ns, p.status, 10, peer_abort))
+            break;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
     }
@@ -434,9 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok)   // copies still in flight complete before the CTA may exit
-      for (int s = 0; s < STAGES; ++s)
-        if ((filled >> s) & 1u) drain_wait(bar_sffull + 8 * s, (fill_phase >> s) & 1u);
+    in_flight[2] = filled;
+    in_flight[3] = fill_phase;
   } else if (warp >= 2 && warp < kFirstEpiWarp) {
     // ---------------------------------------------------------------- scale warps
     // Per stage, each warp stores its quadrant's scales into the stage's TMEM
@@ -514,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool uniform_n = kPair || p.N % BN == 0;
     const uint64_t adesc0 = sdesc_kmajor_sw128(sbase);
     const uint64_t bdesc0 = sdesc_kmajor_sw128(sbase + C::OFF_B);
-    if (p.test_stall && first_unit < total)
+    if (p.test_stall == 1 && first_unit < total)
       ok = wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 6, peer_abort);
     for (int t = first_unit; ok && t < total; t += unit_stride) {
       uint32_t idesc = idesc_nvf4(kPair ? 2 * BM : BM, BN);
@@ -577,12 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else tc_commit(bar_accf);
       aphase ^= 1;
     }
-    if (!ok && issued) {
-      // tensor-core work in flight completes before the tensor memory is freed
-      if constexpr (kPair) tc_commit_pair(bar_aux);
-      else tc_commit(bar_aux);
-      drain_wait(bar_aux, 0);
-    }
+    in_flight[4] = issued;
   } else if (warp >= kFirstEpiWarp && warp < kFirstEpiWarp + kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
@@ -601,7 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar_acce);
       }
     };
-    for (int t = first_unit; t < total; t += unit_stride) {
+    int t = first_unit;
+    if (p.test_stall == 2 && first_unit < total) {
+      wait_bounded(bar_never, 0, abort_flag, p.wait_limit_ns, p.status, 11, peer_abort);
+      t = total;
+    }
+    for (; t < total; t += unit_stride) {
       int e, nb, mb, rows, ncols;
       sch.decode(t, rank, e, nb, mb, rows, ncols);
       if (!wait_bounded(bar_accf, aphase, abort_flag, p.wait_limit_ns, p.status, 4, peer_abort)) break;
@@ -700,6 +693,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (__builtin_expect(*abort_flag != 0, 0)) {   // all roles have ended
+    if (warp == 0 && lane == 0 && in_flight[0]) {
+      // Copies still in flight complete before the CTA may exit. A pair's
+      // copies complete on the even CTA's barriers together with the other
+      // CTA's, whose producer may have stopped before arming or issuing its
+      // part, so a pair waits a fixed time instead: far longer than a copy
+      // takes to land (microseconds), and both CTAs then still pass the exit
+      // handshake, so neither leaves while the other's copies may land.
+      if constexpr (kPair) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < kPairCopyDrainNs) {
+        }
+      } else {
+        for (int s = 0; s < STAGES; ++s)
+          if ((in_flight[0] >> s) & 1u) drain_wait(bar_full + 8 * s, (in_flight[1] >> s) & 1u);
+      }
+    } else if (warp == kCopyWarp && lane == 0) {
+      for (int s = 0; s < STAGES; ++s)
+        if ((in_flight[2] >> s) & 1u) drain_wait(bar_sffull + 8 * s, (in_flight[3] >> s) & 1u);
+    } else if (warp == 1 && lane == 0 && rank == 0 && in_flight[4]) {
+      // tensor-core work in flight completes before the tensor memory is freed
+      if constexpr (kPair) tc_commit_pair(bar_aux);
+      else tc_commit(bar_aux);
+      drain_wait(bar_aux, 0);
+    }
+    __syncthreads();
+  }
   if constexpr (kPair) {
     // neither CTA of the pair leaves (or frees its tensor memory) while the
     // other may still arrive on its barriers or run MMAs into its tensor memory
