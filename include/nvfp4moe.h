@@ -506,7 +506,7 @@ int moe_forward_static(const void* x, const float* router_logits, int64_t T, int
  *   records NVFP4MOE_ERR_INVALID in the device status word. Rows that no entry
  *   names are not written.
  * Leading dimensions in elements, >= K. Accesses are 16 bytes wide where all
- * operands' rows start on 16-byte boundaries, else one element wide. Inputs
+ * operands' rows start on 16-byte boundaries, else in pairs of elements. Inputs
  * and outputs must not overlap. Requires 1 <= k <= 16, T * k < 2^31.
  * Errors: INVALID, UNSUPPORTED, LAUNCH.
  */

@@ -4,9 +4,9 @@
 // Rule, every step one f32 operation: amax over the block; scale = amax / 448
 // and code = E4M3(x * (448 / amax)), rounded to nearest even. A block whose
 // amax is below 2^-100 has scale 0 and codes 0 (448 / amax stays finite above
-// it). An infinity or a NaN in the block becomes its scale (amax is taken on
-// the bit patterns, where NaN > infinity > every number), so that each of its
-// values reads back as NaN, never as a number.
+// it). An infinity or a NaN in the block becomes its scale (the maximum is NaN
+// where either operand is), so that each of its values reads back as NaN, never
+// as a number.
 //
 // Rows: a warp takes 512 consecutive elements of one row, 16 a lane, so that
 // a lane's codes are one 16-byte store, and eight lanes hold a block. Bytes

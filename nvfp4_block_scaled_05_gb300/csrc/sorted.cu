@@ -347,6 +347,23 @@ void launch_nt(const Args& a, int parts, cudaStream_t s) {
 // the blocks' starts are what takes the time: 30000 x 64, k = 2, 17.9 us against
 // 34.0, 8192 x 64, k = 8, 11.8 against 12.5; but 384 columns, k = 8, 26.9 against
 // 26.1. Fewer tokens than 16 an SM are started in time one by one.
+// The bounds are in packs, and F32's packs of four elements behave as the 16-bit
+// types' of eight. F32, the four weighted calls (spread, sum, spread and sum with
+// dots), this rule / the other side of it:
+//   four tokens to a block / one:  30000 x 64, k = 2, 9.2, 9.8, 12.3, 11.3 / 17.3,
+//     17.3, 17.5, 17.3; 8192 x 128, k = 8, 7.5, 5.9, 11.1, 7.5 / 6.7, 6.2, 10.3,
+//     7.5; the far corner of the rule, 30000 x 128, k = 8, 26.5, 33.9, 50.7, 38.1 /
+//     26.6, 26.7, 49.2, 32.3 (BF16, 256 columns: 28.1, 36.7, 61.5, 42.6 / 27.4,
+//     34.6, 58.8, 40.5)
+//   a warp / 64 threads, k = 8:  8192 x 800 46.1, 40.8, 73.8, 45.0 / 43.6, 41.3,
+//     75.3, 48.1; 2000 x 600 7.3, 6.0, 9.4, 5.7 / 7.8, 6.0, 10.6, 7.2
+//   64 / 256 threads for the plain spread:  8192 x 1200, k = 8, 63.0 / 68.5; x 1600
+//     81.5 / 78.4; k = 2, 23.1 / 30.6 and 30.5 / 34.4
+//   with dots, 512 threads for many pairs / 256, k = 8:  32 x 7167 9.5, 6.4 / 10.5,
+//     7.0; 150 x 10001 16.8, 8.2 / 24.6, 9.0 (BF16 13.9, 10.8 / 19.1, 15.5)
+//   with dots, 256 threads for few tokens / as for many, k = 8:  300 x 7168 22.1,
+//     8.5 / 36.7, 20.3; 600 x 4096 28.8, 12.4 / 31.5, 17.1; 600 x 256, the far
+//     corner, 4.6, 4.4 / 3.7, 3.2
 template <typename T, int V, int KM>
 void launch_v(const Args& a, bool spread, bool dot, cudaStream_t s) {
   constexpr int NT = V == 2 && sizeof(T) == 2 ? 128 : 64;
