@@ -14,8 +14,8 @@
 // quantized once and stored k times. Measured: 8192 x 7168 BF16 to 8 experts
 // each 94 us, 6.4 TB/s of 6.76 (a plain copy's); to one place 31.7 us, 5.6
 // TB/s; 8 x 4096 x 7168 BF16 weights 100 us, 7.0 TB/s. The SwiGLU form is near the
-// bound of its arithmetic with 16-bit sources (16384 x 2048 BF16 30.1 us, 5.6
-// TB/s; F32 48.4 us, 6.2 TB/s).
+// bound of its arithmetic with 16-bit sources (16384 x 2048 BF16 29.1 us, 5.8
+// TB/s; F32 44.4 us, 6.8 TB/s).
 #include "common.cuh"
 
 #include <cuda_fp16.h>
@@ -25,7 +25,10 @@ namespace {
 
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTiny = 0x1p-100f;
-constexpr uint32_t kRowWarps = 4;   // to a block (swiglu of 16384 x 2048 F32: 47.8 us, with 8 49.4, with 16 50.4)
+// Warps to a block. SwiGLU, 16384 x 2048 BF16 with 1 / 2 / 4: 35.7, 29.5, 30.1 us,
+// F32 44.2, 44.1, 44.6; rows, 8192 x 7168 BF16: 59.5, 31.6, 30.3.
+template <bool kSwiGLU>
+constexpr uint32_t kRowWarps = kSwiGLU ? 2 : 4;
 
 // 16 consecutive elements as they lie in memory.
 template <typename T>
@@ -137,7 +140,7 @@ __device__ __forceinline__ float rcp(float x) {
 //   g / (1 + exp(-g)) = g/4 / ((1 + exp(-g)) / 4), since the reciprocal
 //   instruction has no results below 2^-126.
 // Where t overflows d is no number, and is taken as one that changes nothing.
-// (16384 x 2048 BF16: 30.1 us; without d 28.8, and up to 2^-18 off; with the
+// (16384 x 2048 BF16: 29.1 us; without d 28.8, and up to 2^-18 off; with the
 // exponential and the division of CUDA's library 45.)
 __device__ __forceinline__ void silu_mul2(float& v0, float& v1, float u0, float u1) {
   constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
@@ -145,12 +148,11 @@ __device__ __forceinline__ void silu_mul2(float& v0, float& v1, float u0, float 
   const uint64_t g = pair(v0, v1);
   const uint64_t t = mul2(g, pair(-kHi));
   const uint64_t rest = fma2(g, pair(kHi), t);                     // -d without the low part of log2(e)
-  const uint64_t k = fma2(g, pair(-kLo), fma2(rest, pair(-(float)kLn2), pair(1.0f)));
+  const uint64_t k = fma2(g, pair(-kLo / 4), fma2(rest, pair(-(float)kLn2 / 4), pair(0.25f)));   // 2^d / 4
   float t0, t1, k0, k1, d0, d1;
   unpair(t, t0, t1);
   unpair(k, k0, k1);
-  const uint64_t e = mul2(pair(ex2(t0), ex2(t1)), pair(fminf(k0, 2.0f), fminf(k1, 2.0f)));
-  unpair(fma2(e, pair(0.25f), pair(0.25f)), d0, d1);
+  unpair(fma2(pair(ex2(t0), ex2(t1)), pair(fminf(k0, 0.5f), fminf(k1, 0.5f)), pair(0.25f)), d0, d1);
   const uint64_t s = mul2(mul2(g, pair(0.25f)), pair(rcp(d0), rcp(d1)));
   unpair(mul2(s, pair(u0, u1)), v0, v1);
 }
@@ -183,11 +185,11 @@ struct RowArgs {
 // kSwiGLU: a source row holds K gate values, then K up values, and what is
 // quantized is gate / (1 + exp(-gate)) * up in f32.
 template <typename T, bool kSwiGLU>
-__global__ void __launch_bounds__(32 * kRowWarps) quantize_rows_fp8_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(32 * kRowWarps<kSwiGLU>) quantize_rows_fp8_kernel(const RowArgs a) {
   const int lane = threadIdx.x & 31;
   // 32 bits: a 64-bit division would cost a lane as much as half its codes
   const uint32_t chunks = (uint32_t)((a.K + 511) / 512);
-  const uint32_t item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const uint32_t item = blockIdx.x * kRowWarps<kSwiGLU> + (threadIdx.x >> 5);
   const int64_t r = item / chunks;
   if (r >= a.rows) return;
   const int64_t col = (int64_t)(item % chunks) * 512 + lane * 16;
@@ -209,11 +211,15 @@ __global__ void __launch_bounds__(32 * kRowWarps) quantize_rows_fp8_kernel(const
   x.zero();
   const T* p = static_cast<const T*>(a.x) + r * a.ldx + col;
   if (valid) x.load(p);
+  Raw16<T> up;   // (on its way before the gate is converted: F32 44.1 us, after it 46.4)
+  if constexpr (kSwiGLU) {
+    up.zero();
+    if (valid) up.load(p + a.K);
+  }
   to_f32(x, v);
   if constexpr (kSwiGLU) {
     float u[16];
-    if (valid) x.load(p + a.K);
-    to_f32(x, u);
+    to_f32(up, u);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) silu_mul2(v[i], v[i + 1], u[i], u[i + 1]);
   }
@@ -294,12 +300,13 @@ int quantize_rows(RowArgs& a, int type, void* stream) {
               NVFP4MOE_ERR_INVALID);
   a.status = device_status_word();
   NVFP4_CHECK(a.status, NVFP4MOE_ERR_LAUNCH);
-  const int64_t items = a.rows * ceil_div(a.K, 512), blocks = ceil_div(items, kRowWarps);
+  const int64_t items = a.rows * ceil_div(a.K, 512), blocks = ceil_div(items, kRowWarps<kSwiGLU>);
   NVFP4_CHECK(items < (1ll << 32) - 8, NVFP4MOE_ERR_UNSUPPORTED);
+  const unsigned threads = 32 * kRowWarps<kSwiGLU>;
   cudaStream_t s = as_stream(stream);
-  if (type == NVFP4MOE_BF16) quantize_rows_fp8_kernel<__nv_bfloat16, kSwiGLU><<<(unsigned)blocks, 32 * kRowWarps, 0, s>>>(a);
-  else if (type == NVFP4MOE_F16) quantize_rows_fp8_kernel<__half, kSwiGLU><<<(unsigned)blocks, 32 * kRowWarps, 0, s>>>(a);
-  else quantize_rows_fp8_kernel<float, kSwiGLU><<<(unsigned)blocks, 32 * kRowWarps, 0, s>>>(a);
+  if (type == NVFP4MOE_BF16) quantize_rows_fp8_kernel<__nv_bfloat16, kSwiGLU><<<(unsigned)blocks, threads, 0, s>>>(a);
+  else if (type == NVFP4MOE_F16) quantize_rows_fp8_kernel<__half, kSwiGLU><<<(unsigned)blocks, threads, 0, s>>>(a);
+  else quantize_rows_fp8_kernel<float, kSwiGLU><<<(unsigned)blocks, threads, 0, s>>>(a);
   return launch_status();
 }
 
