@@ -115,30 +115,62 @@ __device__ __forceinline__ void load_bounds(const Params& p, int32_t* bounds) {
     bounds[e] = p.offsets ? min(max(p.offsets[e], 0), p.M) : e == 0 ? 0 : p.M;
 }
 
-// The prefix sum of the groups' tiles, by one warp, a run of neighbouring groups
-// a lane. Bounds that do not ascend become the largest so far: whatever the
-// offsets hold, the groups have no row in common, there are no more tiles than
-// the host reckons with, and no tile reaches past the operands.
+// Bounds that do not ascend become the largest so far, by one warp: whatever
+// the offsets hold, the groups have no row in common, there are no more tiles
+// than the host reckons with, and no tile reaches past the operands.
+__device__ __forceinline__ void put_in_order(int E, int32_t* bounds) {
+  if ((threadIdx.x & 31) == 0)
+    for (int e = 0; e < E; ++e) bounds[e + 1] = max(bounds[e], bounds[e + 1]);
+  __syncwarp();
+}
+
+// The bounds in order and the prefix sum of the groups' tiles, by one warp, 32
+// groups at a time.
 __device__ __forceinline__ void scan_tiles(const Sched& sch, int32_t* bounds, int32_t* tile_start) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = 0; base < sch.E; base += 32) {
+    const int e = base + lane;
+    int rows = e < sch.E ? bounds[e + 1] - bounds[e] : 0;
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, rows < 0), 0)) {   // (the groups before ascend, and stay as they are)
+      put_in_order(sch.E, bounds);
+      rows = e < sch.E ? bounds[e + 1] - bounds[e] : 0;
+    }
+    const int mt = (rows + sch.tm - 1) / sch.tm;
+    int incl = mt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (e < sch.E) tile_start[e] = (carry + incl - mt) * sch.NT;
+    carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  if (lane == 0) tile_start[sch.E] = carry * sch.NT;
+}
+
+// The same, a run of neighbouring groups a lane: fewer steps (8 rows of 256
+// groups, 7168 x 2048: 26.3 us against 27.8), but in the kernel with 128-row
+// tiles the compiler makes a slower epilogue beside it (4096 x 4096 x 7168 103.7
+// us against 102.5).
+__device__ __forceinline__ void scan_tiles_by_runs(const Sched& sch, int32_t* bounds, int32_t* tile_start) {
   const int lane = threadIdx.x & 31, run = (sch.E + 31) / 32;
   const int e0 = min(lane * run, sch.E), e1 = min(e0 + run, sch.E);
   bool ascending = true;
   int tiles = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int rows = bounds[e + 1] - bounds[e];
-    ascending = ascending && rows >= 0;
-    tile_start[e] = tiles;
-    tiles += (rows + sch.tm - 1) / sch.tm;
-  }
-  if (__builtin_expect(!__all_sync(0xFFFFFFFFu, ascending), 0)) {
-    if (lane == 0)
-      for (int e = 0; e < sch.E; ++e) bounds[e + 1] = max(bounds[e], bounds[e + 1]);
-    __syncwarp();
+  auto count = [&]() {
     tiles = 0;
     for (int e = e0; e < e1; ++e) {
+      const int rows = bounds[e + 1] - bounds[e];
+      ascending = ascending && rows >= 0;
       tile_start[e] = tiles;
-      tiles += (bounds[e + 1] - bounds[e] + sch.tm - 1) / sch.tm;
+      tiles += (rows + sch.tm - 1) / sch.tm;
     }
+  };
+  count();
+  if (__builtin_expect(!__all_sync(0xFFFFFFFFu, ascending), 0)) {
+    put_in_order(sch.E, bounds);
+    count();
   }
   int incl = tiles;
 #pragma unroll
@@ -229,7 +261,9 @@ struct InFlight {
 
 // Waits for the copies (barriers bar_full, one a stage) and MMAs of an aborted
 // CTA. Called by warps 0 (whose lane 0 is the producer) and 1 (the MMA issuer,
-// converged) after a barrier of the CTA that follows all roles.
+// converged) after a barrier of the CTA that follows all roles. The CTA's shared
+// memory lasts until warp 0 is through, its tensor memory until warp 1 is,
+// which frees it.
 __device__ __forceinline__ void drain(const InFlight& f, int warp, int lane, int stages, uint32_t bar_full,
                                       uint32_t bar_aux) {
   if (warp == 0 && lane == 0) {
@@ -786,10 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (__builtin_expect(*abort_flag != 0, 0)) {
-    drain(*in_flight, warp, lane, STAGES, bar_full, bar_aux);
-    __syncthreads();
-  }
+  if (warp < 2 && *abort_flag) drain(*in_flight, warp, lane, STAGES, bar_full, bar_aux);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -929,7 +960,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (p.offsets) {
-    if (warp == 0) scan_tiles(sch, bounds, tile_start);
+    if (warp == 0) scan_tiles_by_runs(sch, bounds, tile_start);
     __syncthreads();
     if (unit < tile_start[p.E]) {   // the same for every CTA of a cluster
       sch.decode(unit, e, nb, row0, rows, ncols);
@@ -1088,10 +1119,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (split > 1) cluster_sync_all();   // every CTA's part stays until all have read it
   tc_fence_before();
   __syncthreads();
-  if (__builtin_expect(gave_up, 0)) {
-    drain(*in_flight, warp, lane, STAGES, bar_full, bar_aux);
-    __syncthreads();
-  }
+  if (gave_up && warp < 2) drain(*in_flight, warp, lane, STAGES, bar_full, bar_aux);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
