@@ -1171,10 +1171,11 @@ int resident_clusters(Kernel kernel, int index, int threads, size_t most, int sp
     cfg.dynamicSmemBytes = most;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      n = -1;
+      return 0;   // (not kept: another call may be answered)
     }
+    if (n <= 0) n = -1;
     slot.store(n, std::memory_order_relaxed);
   }
   return n;
