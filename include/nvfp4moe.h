@@ -680,10 +680,9 @@ size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t K, int64_t I, int E,
  *   y = sum_j w_j (silu(x Wg^T) * (x Wu^T)) Wd^T [+ residual]
  * over the k experts j and weights that moe_route_topk gives a token. Weights as
  * fp8_moe_forward's, but activations are not rounded to 8 bits (nor h): BF16 and
- * F16 ones are taken as they are, F32 ones to 22 bits, h to 22 bits as well, but
- * to 11 for BF16, whose y has 8. (Bits are relative to the element; one far below
- * the largest of its 128 keeps at least 2^-39 of that one, or of 2^-100 where all
- * are smaller.) Sums in f32, y rounded once. Faster than fp8_moe_forward for
+ * F16 ones are taken as they are, F32 ones and h to 22 bits. (Bits are relative to
+ * the element; one far below the largest of its 128 keeps at least 2^-39 of that
+ * one, or of 2^-100 where all are smaller.) Sums in f32, y rounded once. Faster than fp8_moe_forward for
  * about 8 tokens and fewer, slower where an expert has many more.
  *   x          (T, K) of `type` (BF16, F16, F32), leading dimension ldx, 16-byte
  *              aligned rows.  router_logits (T, E) f32.

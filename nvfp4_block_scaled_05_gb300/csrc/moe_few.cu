@@ -19,13 +19,13 @@
 // A row's activations are taken in the weights' blocks of 128: each block is
 // scaled by a power of two that brings its largest magnitude to [2^14, 2^15),
 // and is held as one f16 or as the sum of two. One holds BF16 and F16 inputs
-// exactly (every element above 2^-28 of its block's largest); F32 inputs take
-// two, 22 bits. h is f32 and takes two as well, but one where y is BF16: an
-// element is then off by 2^-11 of its value at most, y by 2^-8, and the layer took
-// 66.0 us for one token of 256 experts 7168/2048 where two parts took 68.8, 146
-// and 162 for 32 tokens that each take all of 8 experts 4096/2048. The block's
-// sums are scaled back with the weights' scale, in f32, and added in f32 in
-// ascending order.
+// exactly (every element above 2^-28 of its block's largest); F32 inputs and h,
+// which is f32, take two, 22 bits, whatever y's type: with one, 11 bits, the sum
+// carried an error that a BF16 y shows where a residual cancels most of it, and y
+// differed from that of f32 sums by 4.9e-4 of its RMS, now by 6e-5. The second part
+// takes 2 us of the 68 for one token of 256 experts 7168/2048, 15 of the 150 to 161
+// for 32 tokens that each take all of 8 experts 4096/2048. The block's sums are scaled back with the weights'
+// scale, in f32, and added in f32 in ascending order.
 //
 // Work: a unit is two tiles of 16 weight rows over the whole K (gate and up rows
 // of the same columns of h, so that one lane holds both; or neighbouring rows of
@@ -48,16 +48,14 @@
 // and ends the layer without a result; a warp that gave up waits for its copies.
 //
 // Measured in BF16, experts' K/I, with the fraction that reading the codes once
-// takes at 6.79 TB/s: 32 tokens of 8 of 256 experts 7168/2048 1099 us (96%), 16 of
-// 128 578 us (94%), four of 64 200 us (89%), one of 256 66 us (79%); one token of 2
-// of 8 experts 128/128 9.0 us, which is two launches, two routings and the hand-over
-// of h: what bounds every small layer. Where experts have more than 8 tokens their
-// entries do: 32 tokens of 2 of 8 experts 4096/2048 take 61 to 66 us (45%).
-// fp8_moe_forward, with activations of 8 bits, takes 53 there, 77 for one token and
-// 1015 to 1056 for 32 of 256 experts 7168/2048.
+// takes at 6.79 TB/s: 32 tokens of 8 of 256 experts 7168/2048 1061 to 1076 us (98%),
+// 16 of 128 550 us (96%), four of 64 185 us (90%), one of 256 68 us (76%); one token
+// of 2 of 8 experts 128/128 9.3 us, which is two launches, two routings and the
+// hand-over of h: what bounds every small layer. Where experts have more than 8
+// tokens their entries do: 32 tokens of 2 of 8 experts 4096/2048 take 69 to 71 us
+// (42%). fp8_moe_forward, with activations of 8 bits, takes 52 there, 77 for one
+// token and 1004 for 32 of 256 experts 7168/2048.
 #include "fp8_rows.cuh"
-
-#include <type_traits>
 
 namespace nvfp4moe {
 namespace {
@@ -970,12 +968,11 @@ struct FewCall {
   cudaStream_t s;
 };
 
-// P of the second kernel's rows, h: 11 bits of an element suffice where y is rounded
-// to BF16's 8, and F16's 11 and F32's 24 get 22.
+// P: f16 numbers to an element of x; h takes two whatever y's type.
 template <typename T, int P>
 int run_few(FewCall& c) {
   NVFP4_TRY((launch_few<T, T, P, false>(c.w1, c.up, c.sms, c.s)));
-  return launch_few<float, T, std::is_same<T, __nv_bfloat16>::value ? 1 : 2, true>(c.w2, c.down, c.sms, c.s);
+  return launch_few<float, T, 2, true>(c.w2, c.down, c.sms, c.s);
 }
 
 }  // namespace
