@@ -776,7 +776,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   };
   // What a unit's sums become.
   auto finish = [&](int x, int tile, const float (&sum)[2][4]) {
-    if (!ok || *gave_up) return;   // (parts may be of a warp that gave up)
+    // (parts may be of a warp that gave up; others set the word at any time, so that lanes
+    // may read it differently, and what follows takes the whole warp)
+    if (__any_sync(0xFFFFFFFFu, !ok || *gave_up)) return;
     const int entry = r.start[x], cols = r.start[x + 1] - entry;
     const bool two = tile + 1 < run.tile1;
 #pragma unroll

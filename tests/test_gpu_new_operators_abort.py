@@ -74,3 +74,19 @@ def test_few_tokens(T, K, I, E, k):
     assert (y == 7).all()
     B.fp8_moe_few_tokens(x, logits, weights, k, y=y)
     assert torch.equal(y, good) and B.nvfp4moe_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("T,K,I,E,k", [(8, 256, 2048, 16, 6), (32, 512, 1024, 4, 4), (20, 1040, 2064, 3, 2)])
+def test_few_tokens_joined_by_a_counter(T, K, I, E, k, dtype):
+    """Warps that end beside others that gave up, in the form whose last unit joins the columns."""
+    x, logits = _randn(1, T, K).to(dtype), _randn(2, T, E)
+    weights = B.prepare_fp8_moe_weights(_randn(3, E, 2 * I, K) * K ** -0.5, _randn(4, E, K, I) * I ** -0.5)
+    good = B.fp8_moe_few_tokens(x, logits, weights, k)
+    y = torch.full_like(good, 7.0)
+    for _ in range(3):
+        with _stalled():
+            B.fp8_moe_few_tokens(x, logits, weights, k, y=y)
+        assert (y == 7).all()
+    B.fp8_moe_few_tokens(x, logits, weights, k, y=y)
+    assert torch.equal(y, good) and B.nvfp4moe_last_device_status() == 0
