@@ -190,6 +190,14 @@ def _dev(t, name):
     return t
 
 
+def _written(*tensors):
+    """The caller's tensors (or None) that a call wrote into: their versions go up, as those of torch's own in-place
+    operations do, so that a backward pass that saved the old contents refuses. (Tensors of inference mode have none.)"""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 # ------------------------------------------------------------------ sizes
 
 def nvfp4_sf_bytes(rows, cols, sf_layout=NVFP4_SF_TILED):
@@ -217,6 +225,7 @@ def nvfp4_sf_to_tiled(sf, rows, cols, sf_layout=NVFP4_SF_TILED, out=None):
         out = torch.empty(batch * per, dtype=torch.uint8, device=sf.device)
     _check(lib().nvfp4_sf_to_tiled(_ptr(sf), batch, rows, cols, sf_layout, _ptr(out), _stream()),
            "nvfp4_sf_to_tiled")
+    _written(out)
     return out
 
 
@@ -227,6 +236,7 @@ def nvfp4_sf_from_tiled(sf_tiled, batch, rows, cols, sf_layout=NVFP4_SF_TILED, o
         out = torch.empty((batch, rows, cols // 16), dtype=torch.uint8, device=sf_tiled.device)
     _check(lib().nvfp4_sf_from_tiled(_ptr(sf_tiled), batch, rows, cols, sf_layout, _ptr(out), _stream()),
            "nvfp4_sf_from_tiled")
+    _written(out)
     return out
 
 
@@ -307,6 +317,7 @@ def nvfp4_quantize(x, gs=None, row_src=None, sf_layout=NVFP4_SF_TILED, rows=None
     _check(lib().nvfp4_quantize(_ptr(x), rows, cols, x.stride(0), _ptr(gs), _ptr(gs_out),
                                 _ptr(row_src), _ptr(codes), _ptr(sf), sf_layout, _ptr(ws), ws_bytes,
                                 _stream()), "nvfp4_quantize")
+    _written(codes, sf, gs_out)
     return codes, sf, gs_out
 
 
@@ -377,6 +388,7 @@ def nvfp4_grouped_gemm(a_codes, a_sf, gs_a, b_codes, b_sf, gs_b, offsets, out=No
     _check(lib().nvfp4_grouped_gemm(_ptr(a_codes), _ptr(a_sf), _ptr(gs_a), a_codes.shape[0],
                                     _ptr(b_codes), _ptr(b_sf), _ptr(gs_b), _ptr(offsets), E, N, K,
                                     _ptr(out), out.stride(0), _stream()), "nvfp4_grouped_gemm")
+    _written(out)
     return out
 
 
@@ -396,6 +408,7 @@ def nvfp4_rmsnorm_rope_quantize(x, gamma, eps, rope_dims, positions, cos_tab, si
                                              _ptr(positions), _ptr(cos_tab), _ptr(sin_tab), max_pos, _ptr(gs),
                                              _ptr(codes), _ptr(sf), sf_layout, _ptr(y_out), _stream()),
            "nvfp4_rmsnorm_rope_quantize")
+    _written(y_out, codes, sf)
     return codes, sf
 
 
@@ -411,6 +424,7 @@ def nvfp4_linear(a_codes, a_sf, gs_a, M, w_codes, w_sf, gs_w, out=None, ws=None)
     _check(lib().nvfp4_linear(_ptr(a_codes), _ptr(a_sf), _ptr(gs_a), M, a_codes.shape[0], _ptr(w_codes),
                               _ptr(w_sf), _ptr(gs_w), N, K, _ptr(out), out.stride(0), _ptr(ws), ws.numel(),
                               _stream()), "nvfp4_linear")
+    _written(out, ws)
     return out
 
 
@@ -428,6 +442,7 @@ def nvfp4_grouped_gemm_swiglu(a_codes, a_sf, gs_a, w1_codes, w1_sf, gs_w1, offse
                                            _ptr(w1_codes), _ptr(w1_sf), _ptr(gs_w1), _ptr(offsets), E,
                                            I, K, _ptr(gs_h), _ptr(h_codes), _ptr(h_sf), _stream()),
            "nvfp4_grouped_gemm_swiglu")
+    _written(h_codes, h_sf)
     return h_codes, h_sf
 
 
@@ -438,6 +453,7 @@ def moe_combine(out, topk_w, flat_to_perm, y=None):
         y = torch.empty((T, K), dtype=torch.bfloat16, device=out.device)
     _check(lib().moe_combine(_ptr(out), out.stride(0), _ptr(topk_w), _ptr(flat_to_perm), T, k, K,
                              _ptr(y), y.stride(0), _stream()), "moe_combine")
+    _written(y)
     return y
 
 
@@ -656,6 +672,7 @@ def fp8_moe_forward(x, logits, weights, k, ws=None, y=None):
     _check(lib().fp8_moe_forward(_ptr(x), _ptr(logits), T, K, I, E, k, _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]),
                                  _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]), _ptr(y), _ptr(ws),
                                  ws.numel() * ws.element_size(), _stream()), "fp8_moe_forward")
+    _written(ws, y)
     return y
 
 
@@ -687,6 +704,7 @@ def moe_forward(x, logits, weights, k, gs_h, ws=None, y=None):
                              _ptr(weights["w1_sf"]), _ptr(weights["gs_w1"]), _ptr(weights["w2_codes"]),
                              _ptr(weights["w2_sf"]), _ptr(weights["gs_w2"]), _ptr(gs_h), _ptr(y),
                              _ptr(ws), ws.numel(), _stream()), "moe_forward")
+    _written(ws, y)
     return y
 
 
@@ -704,6 +722,7 @@ def moe_forward_static(x, logits, weights, k, gs_h, gs_x, ws=None, y=None):
                                     _ptr(weights["w1_codes"]), _ptr(weights["w1_sf"]), _ptr(weights["gs_w1"]),
                                     _ptr(weights["w2_codes"]), _ptr(weights["w2_sf"]), _ptr(weights["gs_w2"]),
                                     _ptr(gs_h), _ptr(y), _ptr(ws), ws.numel(), _stream()), "moe_forward_static")
+    _written(ws, y)
     return y
 
 
@@ -812,6 +831,7 @@ def moe_forward_stages(x, logits, weights, k, gs_h, ws, y, events=None):
     _check(L.moe_combine(p["out"], K, p["topk_w"], p["flat_to_perm"], T, k, K, _ptr(y), y.stride(0), s),
            "combine")
     mark(first + 3)
+    _written(ws, y)
     return y
 
 
@@ -855,4 +875,5 @@ def moe_forward_static_stages(x, logits, weights, k, gs_h, gs_x, ws, y, events=N
     mark(3)
     _check(L.moe_combine(p["out"], K, p["topk_w"], p["flat_to_perm"], T, k, K, _ptr(y), K, s), "combine")
     mark(4)
+    _written(ws, y)
     return y

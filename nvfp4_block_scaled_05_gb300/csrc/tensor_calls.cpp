@@ -158,13 +158,24 @@ Dots dots(PyObject* o, const char* name, int64_t n, int64_t c, const Matrix& lik
 
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
+// `into`: the caller's tensors that the call writes into, or none. Their versions go
+// up, as those of torch's own in-place operations do: a backward pass that saved the
+// old contents then refuses. (A call that is refused has written nothing; tensors of
+// inference mode have no version.)
 template <typename Call>
-void run(const char* what, Call call) {
+void run(const char* what, std::initializer_list<PyObject*> into, Call call) {
   int status;
   void* s = stream();
   Py_BEGIN_ALLOW_THREADS
   status = call(s);
   Py_END_ALLOW_THREADS
+  if (status == NVFP4MOE_OK || status == NVFP4MOE_ERR_LAUNCH) {
+    for (PyObject* o : into) {
+      if (none(o)) continue;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+  }
   if (status != NVFP4MOE_OK) REFUSE("%s failed: %s (%d)", what, nvfp4moe_status_string(status), status);
 }
 
@@ -208,7 +219,7 @@ CALL(moe_sort_tokens, 6)
   const int64_t n = !none(a[4]) ? integer(a[4], "n_rows") : !none(a[5]) ? matrix(a[5], "rows").n : x.n * s.k;
   if (n < 0) REFUSE("n_rows must not be negative");
   const Matrix out = output(a[5], "rows", n, x.c, x.t, x.t.scalar_type());
-  run("moe_sort_tokens", [&](void* st) {
+  run("moe_sort_tokens", {a[5]}, [&](void* st) {
     return ::moe_sort_tokens(x.p, x.type, x.n, x.c, x.ld, s.f2p, s.k, s.w, out.p, n, out.ld, st);
   });
   return wrap(out.t);
@@ -220,7 +231,7 @@ CALL(moe_sort_tokens_backward, 6)
   const Slots s = slots(a[1], a[2], a[3]);
   const Dots w = dots(a[4], "x", s.tokens, d.c, d, s);
   const Matrix out = output(a[5], "dx", s.tokens, d.c, d.t, d.t.scalar_type());
-  run("moe_sort_tokens_backward", [&](void* st) {
+  run("moe_sort_tokens_backward", {a[5]}, [&](void* st) {
     return ::moe_sort_tokens_backward(d.p, d.type, d.n, d.c, d.ld, s.f2p, s.tokens, s.k, s.w, w.p, w.ld, out.p, out.ld,
                                       w.pd, st);
   });
@@ -233,7 +244,7 @@ CALL(moe_unsort_tokens, 5)
   const Matrix r = matrix(a[0], "rows");
   const Slots s = slots(a[1], a[2], a[3]);
   const Matrix out = output(a[4], "y", s.tokens, r.c, r.t, r.t.scalar_type());
-  run("moe_unsort_tokens", [&](void* st) {
+  run("moe_unsort_tokens", {a[4]}, [&](void* st) {
     return ::moe_unsort_tokens(r.p, r.type, r.n, r.c, r.ld, s.f2p, s.tokens, s.k, s.w, out.p, out.ld, st);
   });
   return wrap(out.t);
@@ -251,7 +262,7 @@ CALL(moe_unsort_tokens_backward, 7)
   if (n < 0) REFUSE("n_rows must not be negative");
   const Dots w = dots(a[4], "rows", n, dy.c, dy, s);
   const Matrix out = output(a[6], "d_rows", n, dy.c, dy.t, dy.t.scalar_type());
-  run("moe_unsort_tokens_backward", [&](void* st) {
+  run("moe_unsort_tokens_backward", {a[6]}, [&](void* st) {
     return ::moe_unsort_tokens_backward(dy.p, dy.type, dy.n, dy.c, dy.ld, s.f2p, s.k, s.w, w.p, w.ld, out.p, n, out.ld,
                                         w.pd, st);
   });
@@ -295,7 +306,7 @@ CALL(fp8_quantize, 6)
   const int64_t n = none(a[3]) ? x.n * s.k : integer(a[3], "out_rows");
   if (n < 0) REFUSE("out_rows must not be negative");
   const Quantized q = quantized(a[4], a[5], n, x.c, x.t);
-  run("fp8_quantize", [&](void* st) {
+  run("fp8_quantize", {a[4], a[5]}, [&](void* st) {
     return ::fp8_quantize(x.p, x.type, x.n, x.c, x.ld, s.f2p, s.k, n, q.pc, q.ps, st);
   });
   return pair(q.codes, q.sf);
@@ -306,7 +317,7 @@ CALL(fp8_swiglu_quantize, 3)
   const Matrix x = matrix(a[0], "gate_up");
   if (x.c % 2 != 0) REFUSE("gate_up must have as many up as gate columns");
   const Quantized q = quantized(a[1], a[2], x.n, x.c / 2, x.t);
-  run("fp8_swiglu_quantize", [&](void* st) {
+  run("fp8_swiglu_quantize", {a[1], a[2]}, [&](void* st) {
     return ::fp8_swiglu_quantize(x.p, x.type, x.n, x.c / 2, x.ld, q.pc, q.ps, st);
   });
   return pair(q.codes, q.sf);
@@ -323,7 +334,7 @@ CALL(fp8_quantize_weight, 1)
   at::Tensor codes = at::empty(w.sizes(), w.options().dtype(at::kByte));
   at::Tensor sf = many ? at::empty({E, blocks(N), blocks(K)}, w.options().dtype(at::kFloat))
                        : at::empty({blocks(N), blocks(K)}, w.options().dtype(at::kFloat));
-  run("fp8_quantize_weight", [&](void* st) {
+  run("fp8_quantize_weight", {}, [&](void* st) {
     return ::fp8_quantize_weight(w.data_ptr(), type, E, N, K, K, static_cast<uint8_t*>(codes.data_ptr()),
                                  static_cast<float*>(sf.data_ptr()), st);
   });
@@ -378,7 +389,7 @@ CALL(rms_norm, 6)
   if (recorded(a[0]) || recorded(a[1]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Norm m = norm(a[0], a[1], a[2], a[3], a[5]);
   const Matrix y = output(a[4], "y", m.x.n, m.x.c, m.x.t, m.x.t.scalar_type());
-  run("rms_norm", [&](void* st) {
+  run("rms_norm", {a[4], a[5]}, [&](void* st) {
     return ::rms_norm(m.x.p, m.x.type, m.x.n, m.x.c, m.x.ld, m.r.p, m.r.ld, m.gamma, m.eps, m.h.p, m.h.ld, y.p, y.ld,
                       st);
   });
@@ -395,7 +406,7 @@ CALL(fp8_rms_norm_quantize, 9)
   const Matrix y = with_y || !none(a[5]) ? output(a[5], "y", m.x.n, m.x.c, m.x.t, type)
                                          : optional(a[5], "y", m.x.n, m.x.c, type);
   const Quantized q = quantized(a[7], a[8], m.x.n, m.x.c, m.x.t);
-  run("fp8_rms_norm_quantize", [&](void* st) {
+  run("fp8_rms_norm_quantize", {a[5], a[6], a[7], a[8]}, [&](void* st) {
     return ::fp8_rms_norm_quantize(m.x.p, m.x.type, m.x.n, m.x.c, m.x.ld, m.r.p, m.r.ld, m.gamma, m.eps, m.h.p, m.h.ld,
                                    y.p, y.ld, q.pc, q.ps, st);
   });
@@ -421,7 +432,7 @@ CALL(rms_norm_backward, 6)
   at::Tensor d_gamma = at::empty({dy.c}, dy.t.options().dtype(at::kFloat));
   const int64_t bytes = (int64_t)::rms_norm_backward_workspace_size(dy.n, dy.c);
   at::Tensor ws = at::empty({bytes / 4}, d_gamma.options());
-  run("rms_norm_backward", [&](void* st) {
+  run("rms_norm_backward", {a[5]}, [&](void* st) {
     return ::rms_norm_backward(dy.p, dy.type, dy.n, dy.c, dy.ld, h.p, h.ld, gamma, (float)eps, dh.p, dh.ld, dx.p, dx.ld,
                                static_cast<float*>(d_gamma.data_ptr()), ws.data_ptr(), (size_t)bytes, st);
   });
@@ -445,7 +456,7 @@ CALL(fp8_linear, 6)
   const auto* sx = static_cast<const float*>(flat(a[1], "a_sf", at::kFloat, {x.n, kb}));
   const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, {blocks(w.n), kb}));
   const Matrix out = output(a[4], "out", x.n, w.n, x.t, product_type(a[4], a[5]));
-  run("fp8_linear", [&](void* st) {
+  run("fp8_linear", {a[4]}, [&](void* st) {
     return ::fp8_linear(static_cast<const uint8_t*>(x.p), sx, x.n, x.ld, static_cast<const uint8_t*>(w.p), sw, w.n,
                         x.c, w.ld, out.p, out.type, out.ld, st);
   });
@@ -464,7 +475,7 @@ CALL(fp8_grouped_gemm, 7)
   const auto* sw = static_cast<const float*>(flat(a[3], "w_sf", at::kFloat, {E, blocks(N), kb}));
   const auto* off = static_cast<const int32_t*>(flat(a[4], "offsets", at::kInt, {E + 1}));
   const Matrix out = output(a[5], "out", x.n, N, x.t, product_type(a[5], a[6]));
-  run("fp8_grouped_gemm", [&](void* st) {
+  run("fp8_grouped_gemm", {a[5]}, [&](void* st) {
     return ::fp8_grouped_gemm(static_cast<const uint8_t*>(x.p), sx, x.n, x.ld,
                               static_cast<const uint8_t*>(w.data_ptr()), sw, off, (int)E, N, x.c, x.c, out.p, out.type,
                               out.ld, st);
@@ -507,7 +518,7 @@ CALL(fp8_linear_epilogue, 9)
   const at::ScalarType type = product_type(a[7], a[8]);
   const Matrix r = optional(a[6], "residual", x.n, w.n, type);
   const Matrix out = output(a[7], "out", x.n, w.n, x.t, type);
-  run("fp8_linear_epilogue", [&](void* st) {
+  run("fp8_linear_epilogue", {a[7]}, [&](void* st) {
     return ::fp8_linear_epilogue(static_cast<const uint8_t*>(x.p), sx, x.n, x.ld, static_cast<const uint8_t*>(w.p), sw,
                                  w.n, x.c, w.ld, bias, act, r.p, r.ld, out.p, out.type, out.ld, st);
   });
@@ -545,7 +556,7 @@ CALL(fp8_moe_few_tokens, 10)
     ws = on_gpu(a[8], "ws");
     if (!ws.is_contiguous()) REFUSE("ws must be contiguous");
   }
-  run("fp8_moe_few_tokens", [&](void* st) {
+  run("fp8_moe_few_tokens", {a[8], a[9]}, [&](void* st) {
     return ::fp8_moe_few_tokens(x.p, x.type, T, K, x.ld, logits, I, (int)E, (int)k,
                                 static_cast<const uint8_t*>(w1.data_ptr()), s1,
                                 static_cast<const uint8_t*>(w2.data_ptr()), s2, r.p, r.ld, y.p, y.ld, ws.data_ptr(),
