@@ -105,12 +105,22 @@ void* flat(PyObject* o, const char* name, at::ScalarType type, std::initializer_
   return t.data_ptr();
 }
 
+// No call has a forward-mode derivative: operands with a tangent are refused, and so
+// are outputs, whose tangent would be that of the old contents. (Whether gradients are
+// recorded does not matter: torch.no_grad leaves tangents on.)
+void no_tangents(std::initializer_list<PyObject*> operands) {
+  for (PyObject* o : operands)
+    if (!none(o) && THPVariable_Check(o) && THPVariable_Unpack(o)._fw_grad(0).defined())
+      REFUSE("the call has no forward-mode derivative: give it tensors without tangents");
+}
+
 // The caller's output, or a new one.
 Matrix output(PyObject* o, const char* name, int64_t n, int64_t c, const at::Tensor& like, at::ScalarType type) {
   if (none(o)) {
     at::Tensor t = at::empty({n, c}, like.options().dtype(type));
     return Matrix{t, n, c, c, t.data_ptr(), float_type(type)};
   }
+  no_tangents({o});
   Matrix m = matrix(o, name);
   if (m.n != n || m.c != c || m.t.scalar_type() != type)
     REFUSE("%s must be %lld x %lld of %s", name, (long long)n, (long long)c, c10::toString(type));
@@ -212,6 +222,7 @@ bool recorded(PyObject* o) {
 
 // x, flat_to_perm, k, topk_w, n_rows, rows
 CALL(moe_sort_tokens, 6)
+  no_tangents({a[0], a[3], a[5]});
   if (recorded(a[0]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Matrix x = matrix(a[0], "x");
   const Slots s = slots(a[1], a[2], a[3]);
@@ -227,6 +238,7 @@ END_CALL
 
 // d_rows, flat_to_perm, k, topk_w, x, dx
 CALL(moe_sort_tokens_backward, 6)
+  no_tangents({a[0], a[3], a[4]});
   const Matrix d = matrix(a[0], "d_rows");
   const Slots s = slots(a[1], a[2], a[3]);
   const Dots w = dots(a[4], "x", s.tokens, d.c, d, s);
@@ -240,6 +252,7 @@ END_CALL
 
 // rows, flat_to_perm, k, topk_w, y
 CALL(moe_unsort_tokens, 5)
+  no_tangents({a[0], a[3], a[4]});
   if (recorded(a[0]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Matrix r = matrix(a[0], "rows");
   const Slots s = slots(a[1], a[2], a[3]);
@@ -252,6 +265,7 @@ END_CALL
 
 // dy, flat_to_perm, k, topk_w, rows, n_rows, d_rows
 CALL(moe_unsort_tokens_backward, 7)
+  no_tangents({a[0], a[3], a[4]});
   const Matrix dy = matrix(a[0], "dy");
   const Slots s = slots(a[1], a[2], a[3]);
   if (s.tokens != dy.n) REFUSE("flat_to_perm must have k entries for each row of dy");
@@ -386,6 +400,7 @@ Norm norm(PyObject* x, PyObject* gamma, PyObject* eps, PyObject* residual, PyObj
 
 // x, gamma, eps, residual, y, h
 CALL(rms_norm, 6)
+  no_tangents({a[0], a[1], a[3], a[4], a[5]});
   if (recorded(a[0]) || recorded(a[1]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Norm m = norm(a[0], a[1], a[2], a[3], a[5]);
   const Matrix y = output(a[4], "y", m.x.n, m.x.c, m.x.t, m.x.t.scalar_type());
@@ -398,6 +413,7 @@ END_CALL
 
 // x, gamma, eps, residual, with_y, y, h, codes, sf
 CALL(fp8_rms_norm_quantize, 9)
+  no_tangents({a[0], a[1], a[3], a[5], a[6]});
   if (recorded(a[0]) || recorded(a[1]) || recorded(a[3])) Py_RETURN_NOTIMPLEMENTED;
   const Norm m = norm(a[0], a[1], a[2], a[3], a[6]);
   const int with_y = PyObject_IsTrue(a[4]);
@@ -421,6 +437,7 @@ END_CALL
 
 // dy, h, gamma, eps, dh, dx
 CALL(rms_norm_backward, 6)
+  no_tangents({a[0], a[1], a[2], a[4]});
   const Matrix dy = matrix(a[0], "dy");
   const at::ScalarType type = dy.t.scalar_type();
   const Matrix h = optional(a[1], "h", dy.n, dy.c, type), dh = optional(a[4], "dh", dy.n, dy.c, type);
@@ -507,6 +524,7 @@ int activation(PyObject* o) {
 
 // a_codes, a_sf, w_codes, w_sf, bias, activation, residual, out, out_dtype
 CALL(fp8_linear_epilogue, 9)
+  no_tangents({a[4], a[6]});
   not_recorded("fp8_linear_epilogue", {a[4], a[6]});
   const Matrix x = matrix(a[0], "a_codes", true), w = matrix(a[2], "w_codes", true);
   if (w.c != x.c) REFUSE("a_codes and w_codes must have the same K");
@@ -534,6 +552,7 @@ const at::Tensor& expert_codes(PyObject* o, const char* name) {
 
 // x, logits, w1_codes, w1_sf, w2_codes, w2_sf, k, residual, ws, y
 CALL(fp8_moe_few_tokens, 10)
+  no_tangents({a[0], a[1], a[7]});
   not_recorded("fp8_moe_few_tokens", {a[0], a[1], a[7]});
   const Matrix x = matrix(a[0], "x");
   const at::ScalarType type = x.t.scalar_type();
