@@ -616,7 +616,11 @@ int fp8_moe_forward(const void* x, const float* router_logits, int64_t T, int64_
 /*
  * fp8_linear_epilogue -- fp8_linear with what follows a projection:
  *   C = act(A W^T + bias) + residual
- * in f32, rounded once to c_type. Operands and requirements as fp8_linear.
+ * in f32, rounded once to c_type. Operands and requirements as fp8_linear. An F32
+ * result is fp8_linear's sum and then one addition each for bias and residual. The
+ * f32 sums of a BF16 or F16 one may begin with the bias and, without an activation,
+ * with the residual, which is off that by 2^-24 (ceil(K / 128) + 2) (|bias| +
+ * |residual|) at most, before the rounding to c_type.
  *   bias       (N) f32, 16-byte aligned, or NULL.
  *   activation NVFP4MOE_ACT_NONE; _RELU max(v, 0); _GELU v (1 + erf(v /
  *              sqrt(2))) / 2; _GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715

@@ -594,19 +594,36 @@ __device__ __forceinline__ void add_residual_row(float (&acc)[HN], const T* r, i
   }
 }
 
-// What a row of sums starts with: the bias (in shared memory, or null) and, without an
-// activation, the residual, whose loads are on their way together here, into
-// registers that are free, where after the last block there is room for two
-// (4096 x 7168 x 2048, BF16: 76 us; without a residual 60, fp8_linear 54). The f32
-// sums then carry the residual's magnitude: a rounding of it for each block of K, as
-// a sum of that length has.
+// Whether a row of sums starts with the bias and the residual. The sums then carry
+// their magnitude: a rounding of 2^-24 of it for each block of K, which is below a
+// BF16 or F16 result's own rounding, but not an F32 one's: its sums start at 0 and
+// what follows is added after the last block, in one f32 addition each.
+template <typename T>
+constexpr bool kStartsWith = sizeof(T) == 2;
+
+template <int N>
+__device__ __forceinline__ void add_bias(float (&v)[N], const float4* bias) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 q = bias[i];
+    v[4 * i] += q.x;
+    v[4 * i + 1] += q.y;
+    v[4 * i + 2] += q.z;
+    v[4 * i + 3] += q.w;
+  }
+}
+
+// What a row of 16-bit results' sums starts with: the bias (in shared memory, or null)
+// and, without an activation, the residual, whose loads are on their way together here,
+// into registers that are free, where after the last block there is room for two
+// (4096 x 7168 x 2048, BF16: 76 us; without a residual 60, fp8_linear 54).
 template <typename T, int kMode>
 __device__ __forceinline__ void start_row(const Params& p, float (&acc)[HN], int64_t row, int col, int n, bool in,
                                           const float4* bias) {
   constexpr int PER = 32 / (int)sizeof(T), BATCH = 8;
 #pragma unroll
   for (int i = 0; i < HN; ++i) acc[i] = 0.0f;
-  if (p.split > 1) return;   // the joining CTA does all
+  if (!kStartsWith<T> || p.split > 1) return;   // (with parts the joining CTA does all)
   if (kMode == kSums && p.residual && in) {
     const T* r = static_cast<const T*>(p.residual) + row * p.ldr + col;
     if (p.r_unit == 32 && n == HN) {
@@ -626,16 +643,7 @@ __device__ __forceinline__ void start_row(const Params& p, float (&acc)[HN], int
       add_residual_row(acc, r, n, p.r_unit);
     }
   }
-  if (bias) {
-#pragma unroll
-    for (int i = 0; i < HN / 4; ++i) {
-      const float4 q = bias[i];
-      acc[4 * i] += q.x;
-      acc[4 * i + 1] += q.y;
-      acc[4 * i + 2] += q.z;
-      acc[4 * i + 3] += q.w;
-    }
-  }
+  if (bias) add_bias(acc, bias);
 }
 // The bias of n columns on its way into a warp's 512 bytes of shared memory, 16 of
 // them by each lane; zeros after it.
@@ -652,7 +660,9 @@ __device__ __forceinline__ void expect_row(const Params& p, int64_t row, int col
   for (int i = 0; i < n * (int)sizeof(T); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(c + i));
 }
 template <typename T>
-__device__ __forceinline__ void finish_row(const Params& p, float (&acc)[HN], int64_t row, int col, int n, bool in) {
+__device__ __forceinline__ void finish_row(const Params& p, float (&acc)[HN], int64_t row, int col, int n, bool in,
+                                           const float4* bias) {
+  if (!kStartsWith<T> && bias) add_bias(acc, bias);
   activate(acc, p.act);
   if (p.residual && in)
     add_residual_row(acc, static_cast<const T*>(p.residual) + row * p.ldr + col, n, p.r_unit);
@@ -975,11 +985,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       sch.decode(t, e, nb, row0, rows, ncols);
       const bool live = quad * 32 < rows && col0 < ncols;   // the whole warp
       float acc[HN];
+      // what follows the sums is added after the last block
+      constexpr bool kLast = kMode == kActivated || (kMode == kSums && !kStartsWith<T>);
+      const float4* bias = p.bias ? bias_of + bias_at : nullptr;
       if constexpr (kMode != kPlain) {
         cp_async_wait_all();   // this tile's bias
         __syncwarp();
         start_row<T, kMode>(p, acc, row0 + row, nb * BN + col0, live ? min(HN, ncols - col0) : 0, live && row < rows,
-                            p.bias ? bias_of + bias_at : nullptr);
+                            bias);
         bias_at ^= HN / 4;
         // the next tile's bias is wanted with its first block, and its residual, or this one's after the last
         if (t + stride < total) {
@@ -990,10 +1003,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int n2 = p.N - nb2 * BN - col0;
           if (p.bias) bring_bias(p.bias + nb2 * BN + col0, n2, smem_addr(bias_of + bias_at), lane);
-          if (kMode == kSums && p.residual && row2 + row < p.M && n2 > 0)
+          if (!kLast && p.residual && row2 + row < p.M && n2 > 0)
             expect_row<T>(p, row2 + row, nb2 * BN + col0, min(HN, n2));
         }
-        if (kMode == kActivated && p.residual && split == 1 && live && row < rows)
+        if (kLast && p.residual && split == 1 && live && row < rows)
           expect_row<T>(p, row0 + row, nb * BN + col0, min(HN, ncols - col0));
       } else {
 #pragma unroll
@@ -1038,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       T* out = static_cast<T*>(p.c) + (int64_t)(row0 + quad * 32) * p.ldc + nb * BN + col0;
       const int n = min(HN, ncols - col0);
-      if constexpr (kMode == kActivated) finish_row<T>(p, acc, row0 + row, nb * BN + col0, n, row < rows);
+      if constexpr (kLast) finish_row<T>(p, acc, row0 + row, nb * BN + col0, n, row < rows, bias);
       if constexpr (kWhole) store_rows(out, p.ldc, acc, rows - quad * 32, n, lane);
       else if (row < rows) store_row_shifted(out + lane * p.ldc, acc, n);
     }

@@ -155,3 +155,61 @@ def test_refusals():
             call(a, sa, w, sw, **kw)
     with torch.no_grad():
         call(a, sa, w, sw, bias=bias.clone().requires_grad_())
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("M,N,K", SIZES + [(4096, 640, 7168), (4100, 520, 1040)])
+def test_f32_parts_are_single_additions(M, N, K, act):
+    """An F32 result is fp8_linear's sums, the bias and the residual in one addition each, whatever their size."""
+    a, sa, w, sw, bias, res = _operands(M, N, K, M + N)
+    sums = B.fp8_linear(a, sa, w, sw, out_dtype=F32)
+    far = torch.where(torch.arange(N, device=DEV) % 3 == 0, 2.0 ** 20, 1.0)
+    for b, r in ((bias, None), (None, res), (bias, res), (bias * far, None), (None, res * far), (bias * far, -res * far)):
+        want = sums if b is None else sums + b
+        want = want.clamp_min(0.0) if act == "relu" else want
+        want = want if r is None else want + r
+        got = B.fp8_linear_epilogue(a, sa, w, sw, bias=b, activation=act, residual=r, out_dtype=F32)
+        assert torch.equal(got, want), (b is None, r is None)
+
+
+@pytest.mark.parametrize("M", [3, 300, 2500])
+def test_products_far_below_the_residual(M):
+    """56 blocks of 0.05 beside a residual, or a bias, of 2^20: an F32 result keeps their sum."""
+    N, K = 272, 7168
+    a = torch.zeros(M, K, device=DEV)
+    a[:, ::128] = 0.05
+    w = torch.zeros(N, K, device=DEV)
+    w[:, ::128] = 1.0
+    (a, sa), (w, sw) = B.fp8_quantize(a), B.fp8_quantize_weight(w)
+    sums = (_values(a, sa, 1) @ _values(w, sw, 128).t())
+    for act in ("none", "relu"):
+        res = torch.full((M, N), 2.0 ** 20, device=DEV)
+        got = B.fp8_linear_epilogue(a, sa, w, sw, activation=act, residual=res, out_dtype=F32).double()
+        # half a step of 2^20's f32, and the 56 sums' own roundings
+        assert ((got - 2.0 ** 20 - sums).abs() <= 2.0 ** -4 + 64 * 2.0 ** -24 * sums).all()
+        got = B.fp8_linear_epilogue(a, sa, w, sw, bias=res[0], activation=act, out_dtype=F32).double()
+        assert ((got - 2.0 ** 20 - sums).abs() <= 2.0 ** -4 + 64 * 2.0 ** -24 * sums).all()
+        for dtype in (BF16, F16):        # 2^15 is in F16's range: its step is larger than the products' sum
+            res16 = torch.full((M, N), 2.0 ** 15, dtype=dtype, device=DEV)
+            got = B.fp8_linear_epilogue(a, sa, w, sw, activation=act, residual=res16, out_dtype=dtype).double()
+            want = 2.0 ** 15 + sums
+            assert ((got - want).abs() <= (torch.finfo(dtype).eps / 2 + 64 * 2.0 ** -24) * want).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [5, 300, 2500])
+def test_infinite_residuals(M, act, dtype):
+    """An infinity or NaN of the residual is the result's, and stays in its place."""
+    N, K = 264, 384
+    a, sa, w, sw, bias, res = _operands(M, N, K, 8)
+    res = res.to(dtype)
+    want = B.fp8_linear_epilogue(a, sa, w, sw, bias=bias, activation=act, residual=res, out_dtype=dtype)
+    places = [(0, 0, math.inf), (M - 1, N - 1, -math.inf), (M // 2, 129, math.nan), (M // 2, 7, math.inf)]
+    for i, j, v in places:
+        res[i, j] = v
+    got = B.fp8_linear_epilogue(a, sa, w, sw, bias=bias, activation=act, residual=res, out_dtype=dtype)
+    for i, j, v in places:
+        assert torch.isnan(got[i, j]) if math.isnan(v) else got[i, j] == v
+        got[i, j] = want[i, j]
+    assert torch.equal(got, want)
