@@ -820,7 +820,7 @@ int forward(NormArgs& a, int type, int64_t K, bool quantize, void* stream) {
   if (a.rows == 0 || K == 0) return NVFP4MOE_OK;
   Align al{type_bytes(type), K % kRun == 0 && aligned(a.gamma, 16)};
   NVFP4_CHECK(a.gamma && aligned(a.gamma, 4) && operand_ok(a.x, a.ldx, K, al) &&
-                  (!a.r || (operand_ok(a.r, a.ldr, K, al) && operand_ok(a.h, a.ldh, K, al))) &&
+                  (a.r ? operand_ok(a.r, a.ldr, K, al) && operand_ok(a.h, a.ldh, K, al) : a.h == nullptr) &&
                   (!a.y || operand_ok(a.y, a.ldy, K, al)),
               NVFP4MOE_ERR_INVALID);
   NVFP4_CHECK(quantize ? al.runs && a.codes && a.sf && aligned(a.codes, 16) && aligned(a.sf, 4) : a.y != nullptr,

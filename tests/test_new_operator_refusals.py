@@ -92,3 +92,11 @@ def test_few_tokens(lib):
         args = list(good)
         args[at] = value
         assert lib.fp8_moe_few_tokens(*args) == status, (at, value)
+
+
+@pytest.mark.parametrize("quantize", [False, True])
+def test_norm_h_without_a_residual(lib, quantize):
+    """h is the sum with the residual: given alone it would be left unwritten."""
+    assert _norm(lib, quantize, r=None, ldr=0) == INVALID
+    assert _norm(lib, quantize, r=None, ldr=0, type=1) == INVALID
+    assert _norm(lib, quantize, r=None, rows=0) == OK
