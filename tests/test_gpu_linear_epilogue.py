@@ -213,3 +213,30 @@ def test_infinite_residuals(M, act, dtype):
         assert torch.isnan(got[i, j]) if math.isnan(v) else got[i, j] == v
         got[i, j] = want[i, j]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [3, 2500])
+@pytest.mark.parametrize("act", ACTS)
+def test_small_and_far_arguments(act, M):
+    """Every argument's own bits, down to the smallest, through the bias: no absolute allowance
+    but where the exponential leaves f32's range."""
+    a = torch.zeros(M, 128, dtype=torch.uint8, device=DEV)
+    w = torch.zeros(64, 128, dtype=torch.uint8, device=DEV)
+    sa, sw = torch.ones(M, 1, device=DEV), torch.ones(1, 1, device=DEV)
+    v = torch.tensor([1e-35, 1e-30, 1e-20, 1e-10, 1e-6, 1e-3, 0.03, 0.5, 1.0, 2.0, 3.0, 4.0, 5.5, 7.0, 9.0, 12.0, 15.0, 20.0,
+                      40.0, 80.0, 86.0, 1e3, 1e10, 3e38], device=DEV)
+    bias = torch.zeros(64, device=DEV)
+    bias[:24], bias[24:48] = v, -v
+    got = B.fp8_linear_epilogue(a, sa, w, sw, bias=bias, activation=act, out_dtype=F32).double()
+    if act in ("none", "relu"):
+        assert torch.equal(got, _act(bias.double(), act).expand(M, 64))
+        return
+    b = bias.double()
+    want = _act(b, act)
+    if act == "gelu_tanh":                       # 1 + tanh(u) = 2 sigmoid(2u), without the cancellation
+        want = b * torch.sigmoid(2.0 * math.sqrt(2.0 / math.pi) * (b + 0.044715 * b ** 3))
+    # the exponent, whose factors' and products' roundings (at most 8 of 2^-24) the exponential carries over
+    exponent = {"silu": b.abs(), "gelu": b * b / 2, "gelu_tanh": 1.6 * b.abs() * (1 + 0.045 * b * b)}[act].clamp_max(90.0)
+    # gelu: ten steps of its polynomial, whose coefficients add up to 1.73 of its value; below 2^-126 results are 0
+    off = (2.0 ** -19 + 2.0 ** -21 * exponent) * want.abs() + 87 * 2.0 ** -126
+    assert ((got - want).abs() <= off).all(), float(((got - want).abs() / off).max())
