@@ -619,7 +619,7 @@ int fp8_moe_forward(const void* x, const float* router_logits, int64_t T, int64_
  * in f32, rounded once to c_type. Operands and requirements as fp8_linear. An F32
  * result is fp8_linear's sum and then one addition each for bias and residual. The
  * f32 sums of a BF16 or F16 one may begin with the bias and, without an activation,
- * with the residual, which is off that by 2^-24 (ceil(K / 128) + 2) (|bias| +
+ * with the residual, which moves the sum by 2^-24 (ceil(K / 128) + 2) (|bias| +
  * |residual|) at most, before the rounding to c_type.
  *   bias       (N) f32, 16-byte aligned, or NULL.
  *   activation NVFP4MOE_ACT_NONE; _RELU max(v, 0); _GELU v (1 + erf(v /
@@ -659,10 +659,12 @@ int fp8_linear_epilogue(const uint8_t* a_codes, const float* a_sf, int64_t M, in
  *                aligned; not to be shared by calls in flight.
  * Through 8-bit codes the gradient is that of y, passed straight.
  * Leading dimensions in elements, >= K. rms_norm and its gradient take rows of
- * any width up to 16384 at any alignment, fastest where K is a multiple of 8 and
- * all rows and gamma start on 16-byte boundaries, which fp8_rms_norm_quantize
- * requires, with K a multiple of 16. Sums are f32 in a fixed order: results do
- * not change from call to call. Errors: INVALID, UNSUPPORTED, WORKSPACE, LAUNCH;
+ * any width up to 16384 at any alignment, about twice as fast where K is a multiple
+ * of 8 and all rows and gamma start on 16-byte boundaries (the gradient then of many
+ * rows up to 14336 wide, 8192 in F32), which fp8_rms_norm_quantize requires, with K a
+ * multiple of 16. Sums, of squares too, are f32 in a fixed order: results do not
+ * change from call to call, and a row whose squares add up past f32's range has y =
+ * 0. Errors: INVALID, UNSUPPORTED, WORKSPACE, LAUNCH;
  * a wait that runs out on the device is reported by
  * nvfp4moe_last_device_status, and rows that were not complete are not written.
  */
@@ -687,7 +689,8 @@ size_t fp8_moe_few_tokens_workspace_size(int64_t T, int64_t K, int64_t I, int E,
  * F16 ones are taken as they are, F32 ones and h to 22 bits. (Bits are relative to
  * the element; one far below the largest of its 128 keeps at least 2^-39 of that
  * one, or of 2^-100 where all are smaller.) Sums in f32, y rounded once. Faster than fp8_moe_forward for
- * about 8 tokens and fewer, slower where an expert has many more.
+ * one and two tokens, about as fast for 4 to 8 (faster in small layers), slower where
+ * experts have many more.
  *   x          (T, K) of `type` (BF16, F16, F32), leading dimension ldx, 16-byte
  *              aligned rows.  router_logits (T, E) f32.
  *   w1_codes   (E, 2I, K), rows [gate 0..I-1 | up 0..I-1], w1_sf, w2_codes

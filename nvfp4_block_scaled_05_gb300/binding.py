@@ -7,7 +7,10 @@ raises on a non-zero status. All arithmetic runs in the library's kernels; if
 the library cannot be loaded, every call fails loudly. The calls whose kernels
 take a few microseconds (the sorted tokens, the 8-bit operators) are marshalled
 by the extension module _tensor_calls (csrc/tensor_calls.cpp), the others by
-ctypes.
+ctypes. A call that writes into tensors of the caller's raises their versions, so
+that autograd notices (a replay of a captured graph does not). No call has a
+forward-mode derivative; those that are differentiable, or that refuse to lose a
+gradient, refuse tangents.
 """
 import ctypes
 import os

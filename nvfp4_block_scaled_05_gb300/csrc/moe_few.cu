@@ -9,12 +9,13 @@
 // nothing. Products are mma.sync of f16 operands with f32 sums: E4M3 codes are
 // f16 numbers, and tcgen05 has no form that takes 8-bit weights with wider
 // activations. 16 weight rows are the MMA's M, 8 tokens its N. The loop moves its
-// codes at 6.5 TB/s at most, which is HBM's rate. An expert's tokens beyond 8 are
-// another entry, which reads and converts the weights again. Entries of 16, whose
-// registers leave 8 warps, were slower at every load measured: 91 against 83 us for
-// 32 tokens of 2 of 16 experts 4096/2048, and 171 against 140 where each token takes
-// all of 8. (For the entries of an expert side by side in time, for L2's sake, 162;
-// one copy for both tiles of a unit, or refilled as soon as it is read, the same.)
+// codes at up to 6.7 TB/s, which is HBM's rate. An expert's tokens beyond 8 are
+// another entry, which reads and converts the weights again. (With h of a BF16 result
+// as one f16, see below, entries of 16, whose registers leave 8 warps, were slower at
+// every load measured: 91 against 83 us for 32 tokens of 2 of 16 experts 4096/2048,
+// and 171 against 140 where each token takes all of 8; the entries of an expert side
+// by side in time, for L2's sake, 162; one copy for both tiles of a unit, or refilled
+// as soon as it is read, the same.)
 //
 // A row's activations are taken in the weights' blocks of 128: each block is
 // scaled by a power of two that brings its largest magnitude to [2^14, 2^15),
@@ -67,10 +68,13 @@ constexpr int kTileBytes = 2048;    // 16 rows x 128 codes
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kBlock = 128;
 constexpr int kEntry = 8;           // tokens of an entry
-// 96 KB of codes are on their way to an SM. Time of 32 tokens of 256 experts
-// 7168/2048 in BF16, and of one token, us: 12 warps with 2 stages 1106 and 66.2, 12
-// with 3 1116 and 66.2, 16 with 2 1127 and 66.3, 10 with 3 1081 and 68.1, 8 with 4
-// 1161 and 68.1.
+// 96 KB of codes are on their way to an SM. Time in BF16, us, of one and of 32 tokens
+// of 8 of 256 experts 7168/2048, of 32 tokens of 2 of 8 experts 4096/2048, and of all
+// 8: 12 warps with 2 stages 69.1, 1127, 71 and 164; 12 with 3 68.9, 1136, 98 and 200;
+// 16 with 2 72.5, 1179, 116 and 256; 10 with 3 71.8, 1115, 70 and 179; 8 with 4 70.4,
+// 1270, 77 and 172 (the others have less room for activations, fewer warps, or
+// both). One token of 2 of 8 experts 4096/2048 21.3 to 22.6, 4 of 6 of 64 experts
+// 2048/512 in F16 28.0 to 30.2 with all of them.
 constexpr int kWarps = 12, kStages = 2;
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {

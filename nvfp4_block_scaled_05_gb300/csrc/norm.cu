@@ -291,8 +291,14 @@ constexpr int kMaxStages = 64;
 // residual: 9728 rows of 7168 BF16 105.7 and 85.7, 1216 14.6 and 14.0, 608 8.4 and
 // 9.8; 2432 of 16384 67.0 and 55.0; 9728 of 4096 52.9 and 54.0, of 2048 27.1 and
 // 26.3, of 512 7.4 and 15.9; 4864 of 7168 F32 70.4 and 77.5.
-// Backward, any width: 9728 of 7168 BF16 155.7 (the form for any alignment) and 95.0,
-// 1216 of 1024 10.4 and 10.4, 608 8.4 and 9.9.
+// Backward, 16-bit rows up to 14336 wide and F32 up to 8192 (a row's threads are one
+// group at most; wider rows take the form for any alignment: 2048 of 16384 BF16 97.2).
+// us with dh, that form and copied ahead, for 304, 608, 1216 and 2432 rows: 1024 BF16
+// 6.5 and 9.6, 8.3 and 10.1, 10.5 and 10.6, 14.5 and 13.6; 7168 BF16 12.0 and 12.5,
+// 16.3 and 15.1, 25.4 and 20.6, 46.7 and 31.0; 14336 BF16 16.3 and 18.6, 24.1 and
+// 25.7, 56.9 and 36.5, 101 and 58; 7168 F32 11.9 and 13.4, 17.4 and 18.1, 50.3 and
+// 29.3, 91 and 50. Eight rows an SM is where narrow rows break even; wide ones do
+// between two and six (912 of 7168 F32 36.8 and 24.8).
 constexpr int64_t kWideRow = 6144;
 constexpr int64_t kRowsOfSM = 8;
 
@@ -542,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) rms_norm_backward_rows_kernel(con
 // alike). Which columns a thread has differs from row to row, so that gamma and
 // d_gamma's sums are in shared memory, with a word of padding a piece against bank
 // conflicts, and so is the row between the two passes where there is room.
-// (4096 x 7167 BF16 with a residual 83 us, backward 82, bound by instructions; element
-// by element 145 and 177.)
+// (4096 x 7167 BF16 with a residual 81 us, backward 80, bound by instructions; element
+// by element 145 and 177, aligned rows of 7000 in the other forms 44 and 45.)
 
 template <typename T>
 constexpr int kPiece = 16 / (int)sizeof(T);

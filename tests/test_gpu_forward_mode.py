@@ -1,5 +1,5 @@
-"""Forward-mode derivatives, which none of the calls has: an operand with a tangent is refused, not
-taken as a constant."""
+"""Forward-mode derivatives, which no call has: the calls that are differentiable, or that refuse to
+lose a gradient, refuse an operand with a tangent and do not take it as a constant."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwAD
