@@ -25,8 +25,8 @@
 // carried an error that a BF16 y shows where a residual cancels most of it, and y
 // differed from that of f32 sums by 4.9e-4 of its RMS, now by 6e-5. The second part
 // takes 2 us of the 68 for one token of 256 experts 7168/2048, 15 of the 150 to 161
-// for 32 tokens that each take all of 8 experts 4096/2048. The block's sums are scaled back with the weights'
-// scale, in f32, and added in f32 in ascending order.
+// for 32 tokens that each take all of 8 experts 4096/2048. The block's sums are
+// scaled back with the weights' scale, in f32, and added in f32 in ascending order.
 //
 // Work: a unit is two tiles of 16 weight rows over the whole K (gate and up rows
 // of the same columns of h, so that one lane holds both; or neighbouring rows of

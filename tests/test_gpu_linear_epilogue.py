@@ -240,3 +240,17 @@ def test_small_and_far_arguments(act, M):
     # gelu: ten steps of its polynomial, whose coefficients add up to 1.73 of its value; below 2^-126 results are 0
     off = (2.0 ** -19 + 2.0 ** -21 * exponent) * want.abs() + 87 * 2.0 ** -126
     assert ((got - want).abs() <= off).all(), float(((got - want).abs() / off).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("M,N", [(3, 264), (300, 640), (300, 333), (2000, 4096), (2500, 1031)])
+def test_residuals_in_place(M, N, act, dtype):
+    """A result in its residual's place, wherever the residual is added, again and again the same."""
+    a, sa, w, sw, bias, res = _operands(M, N, 640, 9)
+    res = res.to(dtype)
+    want = B.fp8_linear_epilogue(a, sa, w, sw, bias=bias, activation=act, residual=res, out_dtype=dtype)
+    for _ in range(5):
+        own = res.clone()
+        B.fp8_linear_epilogue(a, sa, w, sw, bias=bias, activation=act, residual=own, out=own)
+        assert torch.equal(own, want)
